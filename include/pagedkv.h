@@ -332,6 +332,54 @@ int paged_reshape_and_cache_fp8(const void* k, const void* v, void* k_cache, voi
                                 int32_t block_size, int64_t num_blocks, int64_t k_token_stride,
                                 int64_t v_token_stride, int dtype, void* stream);
 
+/* The rotary position embedding of a step's queries and keys, and the cache
+ * write of its rotated keys and its values, in one launch.  No passage: the
+ * pages take keys that are already rotated ("MiniPaged-Qwen" §12 writes what
+ * it is given); this is the step between the projections and that write.
+ * For each token t with slot = slot_mapping[t] != -1 and p = positions[t]:
+ *   q_out[t] = rotate(q[t], p); K row of slot = rotate(k[t], p); V row = v[t].
+ * rotate, per head x of head_dim values: the first rot_dim form rot_dim / 2
+ * pairs (a, b), pair i being values (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * when interleaved != 0; with c = cos_sin[p][i], s = cos_sin[p][rot_dim/2 + i]
+ *   a' = a c - b s,  b' = b c + a s,
+ * the two products and their sum each rounded to float32, then once to
+ * dtype; values past rot_dim are copied.  Bit-exact against this definition.
+ *   q, q_out: device [num_tokens, num_heads, head_dim], token t at
+ *     + t * q_token_stride / q_out_token_stride elements, heads of one token
+ *     contiguous.  q_out is q (same pointer and stride: rotated in place) or
+ *     overlaps none of q, k, v.  num_heads 0: no queries (both may be NULL).
+ *   k, v, k_cache, v_cache, slot_mapping, strides, dtype: as for
+ *     paged_reshape_and_cache.
+ *   positions: device int32[num_tokens].
+ *   cos_sin: device float32 [max_positions, rot_dim], row p the cosines of
+ *     position p's rot_dim / 2 angles, then their sines.
+ *   rot_dim: even, 2..head_dim.
+ * slot == -1 marks a padded token: its row of q_out is left as it was.  Any
+ * other slot outside the pool, or a position outside [0, max_positions), is
+ * recorded as KV_ERR_DEVICE_BOUNDS and the token skipped whole.  Any element
+ * alignment; 16-byte aligned rows with head_dim and rot_dim multiples of 16
+ * take the vector kernel.  num_tokens == 0 launches nothing. */
+int paged_rope_and_cache(void* q_out, const void* q, const void* k, const void* v, const int32_t* positions,
+                         const float* cos_sin, void* k_cache, void* v_cache, const int32_t* slot_mapping,
+                         int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t rot_dim, int64_t max_positions, int32_t interleaved, int32_t block_size,
+                         int64_t num_blocks, int64_t q_out_token_stride, int64_t q_token_stride,
+                         int64_t k_token_stride, int64_t v_token_stride, int dtype, void* stream);
+
+/* paged_rope_and_cache into fp8 caches ("paged-attention-impl-detail",
+ * 实践建议 4: the KV cache quantised inside its blocks): the rotated key, as
+ * float32 values before any 16-bit rounding, and the value row are quantised
+ * as paged_reshape_and_cache_fp8 quantises a row (scale amax / 448, E4M3
+ * codes).  q_out is of dtype (fp16 or bf16).  head_dim 64, 128 or 256.  Other
+ * arguments and rules are those of paged_rope_and_cache. */
+int paged_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const void* v, const int32_t* positions,
+                             const float* cos_sin, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                             const int32_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int64_t max_positions,
+                             int32_t interleaved, int32_t block_size, int64_t num_blocks,
+                             int64_t q_out_token_stride, int64_t q_token_stride, int64_t k_token_stride,
+                             int64_t v_token_stride, int dtype, void* stream);
+
 /* paged_decode_attention over fp8 caches and their scales: K_j, V_j are the
  * dequantised rows (the fp8 KV cache of "paged-attention-impl-detail",
  * 实践建议 4, read by MiniPaged-Qwen §13's decode attention).  q and out are fp16 or bf16 (dtype); head_dim 128,

@@ -7,6 +7,8 @@ Public API (all work runs in libpagedkv.so; see include/pagedkv.h):
 * ``reshape_and_cache`` -- CUDA cache write by slot_mapping.
 * ``paged_decode_attention`` -- CUDA single-query GQA attention through
   block tables, with split-K and a log-sum-exp merge.
+* ``rope_and_cache`` / ``rope_and_cache_fp8`` -- rotary embedding of a step's
+  queries and keys with the cache write of its keys and values, one launch.
 * ``paged_decode_step`` -- the step's cache write and decode attention in
   one launch (stream-K kernel), else the two in stream order.
 """
@@ -19,7 +21,8 @@ def __getattr__(name):
     # the kernel wrappers need torch; import them on first use
     if name in ("reshape_and_cache", "reshape_and_cache_layers", "paged_decode_attention", "paged_decode_step", "copy_blocks", "decode_plan",
                 "device_error", "alloc_workspace", "DecodePlan", "reshape_and_cache_fp8",
-                "paged_decode_attention_fp8", "paged_decode_step_fp8", "paged_prefill_attention"):
+                "paged_decode_attention_fp8", "paged_decode_step_fp8", "paged_prefill_attention",
+                "rope_and_cache", "rope_and_cache_fp8"):
         from . import kernels
         return getattr(kernels, name)
     raise AttributeError(name)

@@ -83,6 +83,13 @@ SIGNATURES = {
     "paged_reshape_and_cache_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                             c_int64, c_int32, c_int32, c_int32, c_int64, c_int64, c_int64, c_int,
                                             c_void_p]),
+    "paged_rope_and_cache": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int32,
+                                     c_int64, c_int64, c_int64, c_int64, c_int64, c_int, c_void_p]),
+    "paged_rope_and_cache_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_int32,
+                                         c_int32, c_int64, c_int32, c_int32, c_int64, c_int64, c_int64, c_int64,
+                                         c_int64, c_int, c_void_p]),
     "paged_decode_attention_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                            c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32,
                                            c_int64, c_float, c_int, c_void_p, c_size_t, c_void_p]),

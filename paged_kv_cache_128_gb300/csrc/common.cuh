@@ -31,6 +31,13 @@ template <> struct DType<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
 };
 
+// Two floats to E4M3 codes, nearest-even, saturating; `lo` lands in the low byte.
+__device__ __forceinline__ uint16_t e4m3x2_from(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 inline size_t dtype_bytes(int dtype) { return dtype == KV_DTYPE_F32 ? 4 : 2; }
 
 // Last CUDA error met by an entry point on this thread (see kv_last_cuda_error).

@@ -288,12 +288,6 @@ extern "C" int paged_copy_blocks_fp8(void* k_cache, void* v_cache, float* k_scal
 namespace pagedkv {
 namespace {
 
-__device__ __forceinline__ uint16_t e4m3x2_from(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A read-only 4-byte global load that stays where it is written: volatile,
 // so it is neither dropped nor moved past the slot check into the branch
 // that uses it.

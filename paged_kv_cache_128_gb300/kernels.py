@@ -114,6 +114,113 @@ def reshape_and_cache_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tenso
                                             _stream_ptr(stream)), "paged_reshape_and_cache_fp8")
 
 
+def _same_device(named) -> int:
+    """Index of the one CUDA device that every (tensor, name) is on."""
+    dev = named[0][0].get_device()
+    for t, n in named:
+        d = t.get_device()
+        if d < 0:
+            raise KVError(1, f"{n} must be a CUDA tensor")
+        if d != dev:
+            raise KVError(1, f"{n} is on cuda:{d}, {named[0][1]} on cuda:{dev}")
+    return dev
+
+
+def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping):
+    """Checks shared by the two rotating cache writes; (N, Hq, Hkv, D, bs,
+    NB, q strides)."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous():
+        raise KVError(1, "caches must be contiguous [NB, BS, Hkv, D] of one shape")
+    nb, bs, hkv, d = k_cache.shape
+    n = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int32 or positions.dtype != torch.int32 or positions.numel() != n \
+            or not slot_mapping.is_contiguous() or not positions.is_contiguous():
+        raise KVError(1, "slot_mapping and positions must be contiguous int32 of one length")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise KVError(1, "cos_sin must be contiguous float32 [max_positions, rot_dim]")
+    for t in (k, v):
+        if t.dtype != k.dtype or t.shape != (n, hkv, d) or t.stride(2) != 1 or t.stride(1) != d:
+            raise KVError(1, "k and v must be [N, Hkv, D] of one dtype with dense heads")
+    if q is None:
+        if q_out is not None:
+            raise KVError(1, "q_out without q")
+        return n, 0, hkv, d, bs, nb, 0, 0
+    hq = q.shape[1] if q.dim() == 3 else 0
+    for t in (q, q_out):
+        if t is None or t.dtype != k.dtype or t.shape != (n, hq, d) or t.stride(2) != 1 \
+                or (t.stride(1) != d and hq > 1):
+            raise KVError(1, "q and q_out must be [N, Hq, D] of k's dtype with dense heads")
+    return n, hq, hkv, d, bs, nb, q_out.stride(0), q.stride(0)
+
+
+def rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                   positions: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   slot_mapping: torch.Tensor, interleaved: bool = False,
+                   stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Rotary embedding and cache write in one launch: ``q_out`` becomes q
+    ``[N, Hq, D]`` rotated to ``positions[N]`` (int32), the rotated k and v
+    ``[N, Hkv, D]`` go into the ``[NB, BS, Hkv, D]`` caches at
+    ``slot_mapping[N]`` (-1 = padded token, skipped whole).  ``cos_sin``
+    float32 ``[max_positions, rot_dim]``: cosines, then sines, of each
+    position's angles; value pairs ``(i, i + rot_dim / 2)``, or ``(2i, 2i+1)``
+    if ``interleaved``.  Token strides are free, ``q_out`` may be ``q``; q and
+    q_out ``None``: only k and v."""
+    named = [(k, "k"), (v, "v"), (positions, "positions"), (cos_sin, "cos_sin"), (k_cache, "k_cache"),
+             (v_cache, "v_cache"), (slot_mapping, "slot_mapping")]
+    if q is not None:
+        named += [(q, "q")] + ([(q_out, "q_out")] if q_out is not None else [])
+    dev = _same_device(named)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved,
+                                  stream)
+    n, hq, hkv, d, bs, nb, so, sq = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping)
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise KVError(1, "k, v and the caches must share one dtype")
+    rows, rot = cos_sin.shape
+    check(lib().paged_rope_and_cache(q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(),
+                                     v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), k_cache.data_ptr(),
+                                     v_cache.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, rot, rows,
+                                     1 if interleaved else 0, bs, nb, so, sq, k.stride(0), v.stride(0),
+                                     dtype_code(k.dtype), _stream_ptr(stream)), "paged_rope_and_cache")
+    return q_out
+
+
+def rope_and_cache_fp8(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scales: torch.Tensor, v_scales: torch.Tensor, slot_mapping: torch.Tensor,
+                       interleaved: bool = False,
+                       stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """``rope_and_cache`` into fp8 caches: E4M3 codes ``[NB, BS, Hkv, D]``
+    (uint8) and float32 scales ``[NB, Hkv, BS]``, the rotated key quantised
+    from float32; q, k, v fp16 or bf16."""
+    named = [(k, "k"), (v, "v"), (positions, "positions"), (cos_sin, "cos_sin"), (k_cache, "k_cache"),
+             (v_cache, "v_cache"), (k_scales, "k_scales"), (v_scales, "v_scales"), (slot_mapping, "slot_mapping")]
+    if q is not None:
+        named += [(q, "q")] + ([(q_out, "q_out")] if q_out is not None else [])
+    dev = _same_device(named)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_and_cache_fp8(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, k_scales, v_scales,
+                                      slot_mapping, interleaved, stream)
+    n, hq, hkv, d, bs, nb, so, sq = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping)
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_scales.dtype != torch.float32 \
+            or v_scales.dtype != torch.float32:
+        raise KVError(1, "fp8 caches are uint8 codes with float32 scales")
+    if k_scales.shape != (nb, hkv, bs) or v_scales.shape != (nb, hkv, bs) or not k_scales.is_contiguous() \
+            or not v_scales.is_contiguous():
+        raise KVError(1, "scales must be contiguous [NB, Hkv, BS]")
+    rows, rot = cos_sin.shape
+    check(lib().paged_rope_and_cache_fp8(q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(),
+                                         v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                         slot_mapping.data_ptr(), n, hq, hkv, d, rot, rows, 1 if interleaved else 0,
+                                         bs, nb, so, sq, k.stride(0), v.stride(0), dtype_code(k.dtype),
+                                         _stream_ptr(stream)), "paged_rope_and_cache_fp8")
+    return q_out
+
+
 def paged_decode_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
                                seq_lens: torch.Tensor, scale: float, max_seq_len: int,
