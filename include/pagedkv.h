@@ -144,6 +144,20 @@ int kvbm_take_copies(kvbm_t h, int32_t* src, int32_t* dst, int64_t cap, int64_t*
  * "paged-attention-impl-detail", section Copy-on-Write共享. */
 int kvbm_block_refcount(kvbm_t h, int32_t block, int32_t* out);
 
+/* Groups of a batch's neighbours that share leading blocks, for
+ * paged_decode_attention_shared_prefix ("paged-attention-impl-detail", section
+ * Copy-on-Write共享: the prefix that requests share).  Sequences are taken in
+ * batch order; a group of n sequences sharing p whole blocks (blocks full for
+ * each of them) takes the next one, sharing q <= p blocks with its first, iff
+ * q > 0 and q n >= p (n - 1): iff it then saves no fewer block reads.
+ *   group_start[n + 1]: the groups' bounds in the batch; *num_groups_out + 1
+ *     entries are written, from 0 to n.
+ *   prefix_lens[n]: tokens (whole blocks) each group shares, one entry per group; 0 for a
+ *     group of one.
+ * KV_ERR_UNKNOWN_SEQ if a sequence is not live (nothing written). */
+int kvbm_prefix_groups(kvbm_t h, const int64_t* seq_ids, int64_t n, int32_t* group_start, int32_t* prefix_lens,
+                       int64_t* num_groups_out);
+
 /* *ok = 1 iff one decode append to each listed sequence fits in the free
  * blocks (counts sequences whose next write opens a new block or copies a
  * shared one): can_append_slots of "从零实现一个 mini vLLM: Block
@@ -552,6 +566,49 @@ int paged_decode_attention(void* out, const void* q, const void* k_cache, const 
                            int32_t max_blocks_per_seq, int64_t max_seq_len, float scale,
                            int32_t blocks_per_split, int dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace paged_decode_attention_shared_prefix needs for
+ * these sizes, any grouping and any lengths up to max_seq_len: the pieces of
+ * the groups' and sequences' partial results, and where they lie.  No
+ * passage, as paged_decode_workspace_size. */
+int paged_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int64_t max_seq_len, int dtype, size_t* bytes_out);
+
+/* Decode attention for groups of sequences that share a prefix
+ * ("paged-attention-impl-detail", section Copy-on-Write共享: requests with a
+ * common prompt prefix hold the same physical blocks; kvbm_fork).  The result
+ * is that of paged_decode_attention for every sequence; a group's shared
+ * blocks are read once for all its sequences' queries rather than once per
+ * sequence, and the two parts of a row are joined by log-sum-exp
+ * (MiniPaged-Qwen §17.3).
+ *   group_start: device int32[num_groups + 1], 0 first, num_seqs last, not
+ *     decreasing: group g is sequences group_start[g] .. group_start[g + 1] - 1.
+ *     Anything else is recorded as KV_ERR_DEVICE_BOUNDS and every sequence
+ *     read through its own table.
+ *   prefix_lens: device int32[num_groups].  What is shared is whole blocks: the
+ *     first S_g = floor(min(prefix_lens[g], length of the group's first
+ *     sequence) / bs) entries of the first sequence's table.  Requirement:
+ *     each sequence of the group of length >= S_g * bs has the same S_g first
+ *     entries (kvbm_prefix_groups gives such groups).  Shorter sequences, empty
+ *     ones among them, read their own table.  A negative entry is recorded as
+ *     KV_ERR_DEVICE_BOUNDS and taken as 0.
+ *   num_groups: 0 .. num_seqs; 0: no sharing (both arrays may be NULL).
+ *   workspace: device, >= paged_shared_prefix_workspace_size() bytes, 256-byte
+ *     aligned.  Clobbered; needs no initialisation, and nothing in it outlives
+ *     the call; calls that share one (captured graphs too) must be ordered.
+ * The remaining arguments, their rules and errors are those of
+ * paged_decode_attention.  fp16 and bf16 with head_dim 64 or 128, block_size
+ * 16, 32, 64 or 128, at most 128 query heads per kv head and 4096 sequences
+ * run on the 5th-generation tensor cores (two launches); every other shape
+ * is one paged_decode_attention call.  fp32 accumulation and online softmax,
+ * one rounding to dtype. */
+int paged_decode_attention_shared_prefix(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* seq_lens,
+                                         const int32_t* group_start, const int32_t* prefix_lens, int32_t num_seqs,
+                                         int32_t num_groups, int32_t num_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                         int32_t max_blocks_per_seq, int64_t max_seq_len, float scale, int dtype,
+                                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* One decode step's device work in one call: the cache write of the step's
  * new tokens (exactly as paged_reshape_and_cache) followed by decode

@@ -58,6 +58,7 @@ SIGNATURES = {
     "kvbm_fork": (c_int, [c_void_p, c_int64, c_int64, c_int64]),
     "kvbm_take_copies": (c_int, [c_void_p, P32, P32, c_int64, P64]),
     "kvbm_block_refcount": (c_int, [c_void_p, c_int32, P32]),
+    "kvbm_prefix_groups": (c_int, [c_void_p, P64, c_int64, P32, P32, P64]),
     "kvbm_can_append_slots": (c_int, [c_void_p, P64, c_int64, POINTER(c_int)]),
     "kvbm_decode_step": (c_int, [c_void_p, P64, c_int64, c_int64, P32, P32, P32]),
     "kvbm_prepare_step": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
@@ -111,6 +112,12 @@ SIGNATURES = {
     "paged_decode_attention": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
                                        c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int64, c_float,
                                        c_int32, c_int, c_void_p, c_size_t, c_void_p]),
+    "paged_shared_prefix_workspace_size": (c_int, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int,
+                                                   POINTER(c_size_t)]),
+    "paged_decode_attention_shared_prefix": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                     c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                     c_int32, c_int64, c_int32, c_int64, c_float, c_int, c_void_p,
+                                                     c_size_t, c_void_p]),
     "paged_decode_step": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64,
                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
                                   c_int32, c_int32, c_int64, c_int32, c_int64, c_float, c_int, c_void_p, c_size_t,

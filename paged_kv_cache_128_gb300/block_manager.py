@@ -149,6 +149,19 @@ class KVBlockManager:
         check(self._lib.kvbm_block_refcount(self._h, block, ctypes.byref(out)), "kvbm_block_refcount")
         return out.value
 
+    def prefix_groups(self, seq_ids) -> Tuple[np.ndarray, np.ndarray]:
+        """Groups of neighbours in ``seq_ids`` that share leading blocks
+        (kvbm_prefix_groups): their bounds int32 ``[groups + 1]`` and the
+        tokens each shares int32 ``[groups]``, the ``group_start`` and
+        ``prefix_lens`` of ``paged_decode_attention_shared_prefix``."""
+        ids = _ids(seq_ids)
+        start = np.empty(ids.size + 1, dtype=np.int32)
+        prefix = np.empty(max(1, ids.size), dtype=np.int32)
+        n = ctypes.c_int64()
+        check(self._lib.kvbm_prefix_groups(self._h, _i64(ids), ids.size, _i32(start), _i32(prefix), ctypes.byref(n)),
+              "kvbm_prefix_groups")
+        return start[:n.value + 1].copy(), prefix[:n.value].copy()
+
     # -- queries -----------------------------------------------------------------------
     def num_free_blocks(self) -> int:
         n = ctypes.c_int64()

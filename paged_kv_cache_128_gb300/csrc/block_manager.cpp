@@ -403,6 +403,36 @@ int kvbm_block_refcount(kvbm_t h, int32_t block, int32_t* out) {
   return KV_OK;
 }
 
+int kvbm_prefix_groups(kvbm_t h, const int64_t* seq_ids, int64_t n, int32_t* group_start, int32_t* prefix_lens,
+                       int64_t* num_groups_out) {
+  if (!h || n < 0 || n > INT32_MAX || (n > 0 && (!seq_ids || !prefix_lens)) || !group_start || !num_groups_out)
+    return KV_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i)
+    if (!h->find(seq_ids[i])) return KV_ERR_UNKNOWN_SEQ;
+  int64_t groups = 0;
+  group_start[0] = 0;
+  for (int64_t i = 0; i < n;) {
+    const Sequence& lead = *h->find(seq_ids[i]);
+    int64_t shared = lead.length / h->block_size;  // whole blocks that all members so far have in common
+    int64_t j = i + 1;
+    for (; j < n; ++j) {
+      const Sequence& s = *h->find(seq_ids[j]);
+      const int64_t most = std::min(shared, s.length / h->block_size);
+      int64_t q = 0;
+      while (q < most && s.table[static_cast<size_t>(q)] == lead.table[static_cast<size_t>(q)]) ++q;
+      // the first neighbour only has to share something
+      const int64_t members = j - i;
+      if (q == 0 || q * members < shared * (members - 1)) break;
+      shared = q;
+    }
+    prefix_lens[groups] = j - i > 1 ? static_cast<int32_t>(shared * h->block_size) : 0;
+    group_start[++groups] = static_cast<int32_t>(j);
+    i = j;
+  }
+  *num_groups_out = groups;
+  return KV_OK;
+}
+
 int kvbm_can_append_slots(kvbm_t h, const int64_t* seq_ids, int64_t n, int* ok) {
   if (!h || !ok || n < 0 || (n > 0 && !seq_ids)) return KV_ERR_INVALID_ARG;
   int64_t need = 0;

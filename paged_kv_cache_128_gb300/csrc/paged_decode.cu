@@ -2247,6 +2247,7 @@ using namespace pagedkv;
 extern "C" int pagedkv_internal_reshape_error(int reset, int* code);
 extern "C" int pagedkv_internal_prefill_error(int reset, int* code);
 extern "C" int pagedkv_internal_rope_error(int reset, int* code);
+extern "C" int pagedkv_internal_shared_error(int reset, int* code);
 extern "C" int paged_reshape_and_cache(const void* k, const void* v, void* k_cache, void* v_cache,
                                        const int32_t* slot_mapping, int64_t num_tokens, int32_t num_kv_heads,
                                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
@@ -2648,7 +2649,10 @@ extern "C" int kv_device_error(int reset, int* status_out) {
   int g = 0;
   r = pagedkv_internal_rope_error(reset, &g);
   if (r != KV_OK) return r;
-  *status_out = a ? a : (c ? c : (f ? f : g));
+  int s = 0;
+  r = pagedkv_internal_shared_error(reset, &s);
+  if (r != KV_OK) return r;
+  *status_out = a ? a : (c ? c : (f ? f : (g ? g : s)));
   return KV_OK;
 }
 

@@ -318,29 +318,6 @@ struct TcLayout {
   static constexpr int kSmem = kBytes + 1024;  // slack for 1024-byte alignment
 };
 
-// Three-input max (one instruction on sm_100 and later).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// One key pair of the softmax pass: the running maxima (two chains), P =
-// exp2(e) for both keys rounded to T and packed into s[i] (the pair's S
-// values, at s[2i] and s[2i + 1], are already read), their sum into ls[i % 2].
-template <typename T>
-__device__ __forceinline__ void softmax_pair(float2 e, int i, float& ma, float& mb, uint64_t (&ls)[2],
-                                             uint32_t (&s)[64]) {
-  if (i & 1) mb = max3(mb, e.x, e.y);
-  else ma = max3(ma, e.x, e.y);
-  const uint32_t pk = Mma<T>::pack(fast_exp2(e.x), fast_exp2(e.y));
-  s[i] = pk;
-  // the sum is taken over the rounded P that P V multiplies, so that the
-  // weights the output is normalised by are the ones it was built from
-  const float2 r = Mma<T>::unpack(pk);
-  ls[i & 1] = tc::fadd2(ls[i & 1], tc::f2(r.x, r.y));
-}
-
 // Compiler barrier: the 32 packed values, the sums and the max are computed
 // here, before any later tensor-memory load is issued.
 __device__ __forceinline__ void pin_regs(uint32_t (&v)[32], uint64_t (&ls)[2], float& m) {

@@ -1,7 +1,8 @@
 // Thin inline-PTX wrappers for the 5th-generation tensor cores (sm_100
 // family): tensor-memory allocation, shared-memory matrix descriptors,
 // kind::f16 MMAs with fp32 accumulators in tensor memory, commits to
-// mbarriers, tensor-memory loads and stores, and packed fp32x2 arithmetic.
+// mbarriers, tensor-memory loads and stores, packed fp32x2 arithmetic, and
+// the softmax step of one pair of scores that the attention kernels share.
 #pragma once
 
 #include "common.cuh"
@@ -175,4 +176,28 @@ __device__ __forceinline__ void st_32x32b_x32(uint32_t taddr, const uint32_t* v)
 }
 
 }  // namespace tc
+
+// Three-input max (one instruction on sm_100 and later).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One key pair of the softmax pass: the running maxima (two chains), P =
+// exp2(e) for both keys rounded to T and packed into s[i] (the pair's S
+// values, at s[2i] and s[2i + 1], are already read), their sum into ls[i % 2].
+template <typename T>
+__device__ __forceinline__ void softmax_pair(float2 e, int i, float& ma, float& mb, uint64_t (&ls)[2],
+                                             uint32_t (&s)[64]) {
+  if (i & 1) mb = max3(mb, e.x, e.y);
+  else ma = max3(ma, e.x, e.y);
+  const uint32_t pk = Mma<T>::pack(fast_exp2(e.x), fast_exp2(e.y));
+  s[i] = pk;
+  // the sum is taken over the rounded P that P V multiplies, so that the
+  // weights the output is normalised by are the ones it was built from
+  const float2 r = Mma<T>::unpack(pk);
+  ls[i & 1] = tc::fadd2(ls[i & 1], tc::f2(r.x, r.y));
+}
+
 }  // namespace pagedkv

@@ -438,6 +438,70 @@ def paged_decode_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     return out
 
 
+def shared_prefix_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                            max_seq_len: int, dtype: torch.dtype, device) -> Optional[torch.Tensor]:
+    """Workspace of ``paged_decode_attention_shared_prefix`` for these sizes
+    and any grouping (None when it needs none)."""
+    with torch.cuda.device(device):
+        n = ctypes.c_size_t()
+        check(lib().paged_shared_prefix_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                       max_seq_len, dtype_code(dtype), ctypes.byref(n)),
+              "paged_shared_prefix_workspace_size")
+        return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+
+
+def paged_decode_attention_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                         v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                         group_start: torch.Tensor, prefix_lens: torch.Tensor, scale: float,
+                                         max_seq_len: int, workspace: Optional[torch.Tensor] = None,
+                                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``paged_decode_attention`` where sequences ``group_start[g] ..
+    group_start[g + 1] - 1`` share the blocks of their first
+    ``prefix_lens[g]`` tokens (int32, ``[groups + 1]`` and ``[groups]``; see
+    ``KVBlockManager.prefix_groups``), which are read once for the group.
+    ``workspace``: ``shared_prefix_workspace(...)`` (allocated here if
+    omitted)."""
+    dev = _same_device(((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
+                        (block_tables, "block_tables"), (seq_lens, "seq_lens"), (group_start, "group_start"),
+                        (prefix_lens, "prefix_lens")))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_decode_attention_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, group_start,
+                                                        prefix_lens, scale, max_seq_len, workspace, stream)
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise KVError(1, "q, out and caches must be contiguous")
+    for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (group_start, "group_start"),
+                 (prefix_lens, "prefix_lens")):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise KVError(1, f"{n} must be contiguous int32")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise KVError(1, "q [B, Hq, D], caches [NB, BS, Hkv, D]")
+    B, hq, d = q.shape
+    nb, bs, hkv, d2 = k_cache.shape
+    dt = q.dtype
+    if d2 != d or out.shape != q.shape or v_cache.shape != k_cache.shape or out.dtype != dt or k_cache.dtype != dt \
+            or v_cache.dtype != dt:
+        raise KVError(1, "shape or dtype mismatch")
+    groups = prefix_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B \
+            or group_start.numel() != groups + 1:
+        raise KVError(1, "block_tables [B, max_blocks], seq_lens [B], group_start [groups + 1], prefix_lens [groups]")
+    if workspace is None:
+        workspace = shared_prefix_workspace(B, hq, hkv, d, bs, max_seq_len, dt, q.device)
+        if workspace is not None and stream is not None:
+            workspace.record_stream(stream)  # its memory is not handed out again while that stream may use it
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise KVError(1, "workspace must be contiguous on q's device")
+    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
+    check(lib().paged_decode_attention_shared_prefix(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), group_start.data_ptr(), prefix_lens.data_ptr(), B, groups, hq, hkv, d, bs, nb,
+        block_tables.shape[1], max_seq_len, float(scale), dtype_code(dt), ws_ptr, ws_bytes, _stream_ptr(stream)),
+        "paged_decode_attention_shared_prefix")
+    return out
+
+
 def paged_decode_step(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                       slot_mapping: torch.Tensor, new_token_row: torch.Tensor, k_cache: torch.Tensor,
                       v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
