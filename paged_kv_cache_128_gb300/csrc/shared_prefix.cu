@@ -205,6 +205,13 @@ __device__ __forceinline__ int sp_cta_of(int64_t t, int64_t W, int P) {
   return static_cast<int>(((t + 1) * P + W - 1) / W - 1);
 }
 
+// 32-byte store: a thread's piece of its row is a whole sector.
+__device__ __forceinline__ void st_global_32b(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ int sp_len(const SpParams& p, int b) {
   int L = __ldg(p.seq_lens + b);
   const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
@@ -265,11 +272,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   }
   if (warp == kSpMmaWarp) tc::alloc(tmem_slot, kSpCols);
 
-  // ---- the line: lengths, groups, costs, their prefix sums
+  // ---- the line: lengths, groups, costs, their prefix sums (all global
+  // loads before the first barrier)
   int bad = 0;
   for (int g = tid; NG > 0 && g <= NG; g += kSpThreads) {
-    const int s = __ldg(p.group_start + g);
-    const int nx = g < NG ? __ldg(p.group_start + g + 1) : B;
+    const int s = __ldg(p.group_start + g), nx = g < NG ? __ldg(p.group_start + g + 1) : B;
+    if (g < NG) ln.prefix[g] = __ldg(p.prefix_lens + g);
     ln.start[g] = s;
     if (s < 0 || s > nx || nx > B || (g == 0 && s != 0) || (g == NG && s != B)) bad = 1;
   }
@@ -280,13 +288,9 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     int P = 0, cost = 0;
     if (!bad) {
       const int n = ln.start[g + 1] - ln.start[g];
+      if (ln.prefix[g] < 0) record_error(KV_ERR_DEVICE_BOUNDS);
       if (n > 1) {  // a group of one shares with nobody
-        P = __ldg(p.prefix_lens + g);
-        if (P < 0) {
-          record_error(KV_ERR_DEVICE_BOUNDS);
-          P = 0;
-        }
-        P = min(P, ln.len[ln.start[g]]) / bs * bs;
+        P = max(0, min(ln.prefix[g], ln.len[ln.start[g]])) / bs * bs;
         if (P > 0)
           cost = (n + p.tile_seqs - 1) / p.tile_seqs * ((P + kSpKeys - 1) / kSpKeys + kSpUnitCost);
       }
@@ -343,37 +347,50 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   const int P = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W)), pid = blockIdx.x;
   const int64_t x0 = pid < P ? pid * W / P : 0, x1 = pid < P ? (pid + 1) * W / P : 0;
 
+  // the merge kernel may be launched into what this one leaves free; it waits
+  // for this grid's end itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (x0 < x1) {
     SpWalk walk(p, ln, x0, x1);
-    SpUnit s, ns;
+    SpUnit s;
     if (warp == kSpTmaWarp) {
       // ---- K and V tiles, one box of up to 64 rows per (block, 64-dim slab)
       const int rpc = min(bs, kSpKeys);  // rows of a box
       const int ci = lane / kSlabs, slab = lane % kSlabs;
-      // row of the pool where this lane's box of tile t begins (-1: none)
-      auto pool_row = [&](const SpUnit& un, int t) -> int {
+      // table entry of this lane's box of tile t and the box's offset in the
+      // block (-1: no box); the entry is looked at only when the box is copied
+      auto entry = [&](const SpUnit& un, int t, int& off) -> int {
         const int tok = un.key0 + t * kSpKeys + ci * rpc;
-        if (ci * rpc >= kSpKeys || tok >= un.key1) return -1;
-        int pb = __ldg(p.block_tables + static_cast<int64_t>(un.b0) * p.max_blocks_per_seq + tok / bs);
-        if (pb < 0 || pb >= p.num_blocks) {
+        off = -1;
+        if (ci * rpc >= kSpKeys || tok >= un.key1) return 0;
+        const int blk = tok / bs;
+        off = tok - blk * bs;
+        return __ldg(p.block_tables + static_cast<int64_t>(un.b0) * p.max_blocks_per_seq + blk);
+      };
+      // advances (unit, tile); false past the share's end
+      auto step = [&](SpUnit& un, int& t) -> bool {
+        if (++t < un.t1) return true;
+        if (!walk.next(un)) return false;
+        t = un.t0;
+        return true;
+      };
+      // the table entries of two tiles are in flight ahead of their copies
+      bool more = walk.next(s);
+      int t = s.t0, ok = 1, i = 0;
+      int off = -1, off1 = -1, off2 = -1;
+      int pb = more ? entry(s, t, off) : 0, kvh = s.kvh;
+      bool more1 = more && step(s, t);
+      int pb1 = more1 ? entry(s, t, off1) : 0, kvh1 = s.kvh;
+      while (more && ok) {
+        const bool more2 = more1 && step(s, t);
+        off2 = -1;
+        const int pb2 = more2 ? entry(s, t, off2) : 0, kvh2 = s.kvh;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, off >= 0));
+        if (off >= 0 && (pb < 0 || pb >= p.num_blocks)) {
           record_error(KV_ERR_DEVICE_BOUNDS);
           pb = 0;
         }
-        return pb * bs + tok % bs;
-      };
-      bool more = walk.next(s);
-      int t = s.t0, row = more ? pool_row(s, t) : -1, ok = 1, i = 0;
-      while (more && ok) {
-        // the next tile's table entries are fetched ahead
-        ns = s;
-        int nt = t + 1;
-        bool nmore = true;
-        if (nt == s.t1) {
-          nmore = walk.next(ns);
-          nt = ns.t0;
-        }
-        const int nrow = nmore ? pool_row(ns, nt) : -1;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const int row = pb * bs + off;
         for (int v = 0; v < 2 && ok; ++v, ++i) {
           const int st = i % nst;
           if (lane == 0) {
@@ -381,14 +398,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             if (ok) mbar_arrive_expect_tx(bar_full + st, static_cast<uint32_t>(boxes * rpc * 128));
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok && row >= 0)
+          if (ok && off >= 0)
             tma_load_3d(ring + st * Lay::kTile + slab * Lay::kSlab + ci * rpc * 128, v ? &tmV : &tmK, bar_full + st,
-                        slab * 64, s.kvh, row);
+                        slab * 64, kvh, row);
         }
-        s = ns;
-        t = nt;
-        row = nrow;
-        more = nmore;
+        pb = pb1, off = off1, kvh = kvh1, more = more1;
+        pb1 = pb2, off1 = off2, kvh1 = kvh2, more1 = more2;
       }
       // every stage's last MMAs have completed: no copy or commit in flight at exit
       if (lane == 0 && ok)
@@ -458,26 +473,60 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       const uint64_t c2x2 = tc::f2(c2, c2);
       constexpr float kSlack = 8.f, kLow = 8.f;  // as the prefill: P stays <= 2^8, and not all tiny
       bool ok = true;
-      auto load_q = [&](const SpUnit& un) {
-        constexpr int kCh = D / 8;  // 16-byte chunks of a row
-        for (int i = tid; i < un.rows * kCh; i += kSpSoftWarps * 32) {
-          const int row = i / kCh, ch = i % kCh;
-          const int b = un.b0 + row / p.group, h = un.kvh * p.group + row % p.group;
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-              static_cast<const T*>(p.q) + (static_cast<int64_t>(b) * p.num_heads + h) * D + ch * 8));
-          *reinterpret_cast<uint4*>(sm + (ch >> 3) * Lay::kQSlab + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+      // A unit's Q goes to shared memory in the MMA's swizzled layout, 16-byte
+      // chunk i of the rows by thread i mod 128, loads in batches of kQBatch.
+      // The first batch (all of a rest unit's Q when G D <= 2048) is fetched
+      // while the unit before is still at work.
+      constexpr int kCh = D / 8, kQBatch = 2;
+      uint4 qv[kQBatch];
+      auto fetch_q = [&](const SpUnit& un, int i0) {
+#pragma unroll
+        for (int k = 0; k < kQBatch; ++k) {
+          const int i = i0 + k * kSpSoftWarps * 32;
+          if (i < un.rows * kCh) {
+            const int row = i / kCh, sq = row / p.group;
+            qv[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                         (static_cast<int64_t>(un.b0 + sq) * p.num_heads +
+                                                          un.kvh * p.group + row - sq * p.group) * D) +
+                          i % kCh);
+          }
+        }
+      };
+      auto store_q = [&](const SpUnit& un) {
+        for (int i0 = tid;; ) {
+#pragma unroll
+          for (int k = 0; k < kQBatch; ++k) {
+            const int i = i0 + k * kSpSoftWarps * 32;
+            if (i < un.rows * kCh) {
+              const int row = i / kCh, ch = i % kCh;
+              *reinterpret_cast<uint4*>(sm + (ch >> 3) * Lay::kQSlab + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                  qv[k];
+            }
+          }
+          i0 += kQBatch * kSpSoftWarps * 32;
+          if (i0 >= un.rows * kCh) break;
+          fetch_q(un, i0);
         }
         fence_proxy_async_smem();  // read by the tensor cores
         mbar_arrive(bar_q);
       };
       bool more = walk.next(s);
-      if (more) load_q(s);
+      if (more) {
+        fetch_q(s, tid);
+        store_q(s);
+      }
       int j = 0;
       while (more) {
         const bool mine = warp * 32 < s.rows, valid = r < s.rows;
+        SpUnit nx;
+        bool nmore = false;
         float m_ref = 0.f, l = 0.f;
         for (int t = s.t0; t < s.t1; ++t, ++j) {
           const int buf = (j & 1) * 64;
+          if (t + 1 == s.t1) {
+            nmore = walk.next(nx);
+            if (nmore) fetch_q(nx, tid);
+          }
           // after a timeout (recorded) the remaining waits are skipped
           if (ok && !mbar_wait_bounded(bar_s + (j & 1), (j >> 1) & 1)) ok = false;
           tc::fence_after();
@@ -571,8 +620,11 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         // the last P V runs
         const SpUnit d = s;
         const float m_out = m_ref, l_out = l;
-        more = walk.next(s);
-        if (more) load_q(s);
+        more = nmore;
+        if (more) {
+          s = nx;
+          store_q(s);
+        }
         if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
         tc::fence_after();
         const bool whole = d.t0 == 0 && d.t1 == d.T;
@@ -603,8 +655,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
               }
             } else if (valid) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                reinterpret_cast<uint4*>(po + oc)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              for (int k = 0; k < 32; k += 8) st_global_32b(po + oc + k, w + k);
             }
           }
           if (valid && !direct) *reinterpret_cast<float2*>(pml) = make_float2(m_out, l_out);
@@ -629,89 +680,106 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   }
 }
 
-// Joins a row's pieces: one warp per (sequence, query head), a lane per piece
-// for the statistics, then a lane per D / 32 outputs.  Rows that the first
-// kernel wrote whole are left alone; a sequence of no tokens gets zeros.
-constexpr int kSpMergeWarps = 4;
+// Joins a row's pieces.  WPR warps per (sequence, query head): warp w of them
+// takes pieces w, w + WPR, ..., a lane D / 32 outputs, and the first one adds
+// up the others' in order.  A piece's statistics and its values are loaded
+// together, so a row costs two round trips (where its pieces lie, what they
+// hold).  Rows that the first kernel wrote whole are left alone; a sequence
+// of no tokens gets zeros.  Launched early (programmatic dependent launch): it
+// waits for the first kernel's end before it reads anything.
+constexpr int kSpMergeWarps = 8;
 
-template <typename T, int D>
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const SpParams p) {
-  constexpr int kV = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kSpMergeWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(p.num_seqs) * p.num_heads) return;
-  const int b = static_cast<int>(row / p.num_heads), h = static_cast<int>(row % p.num_heads);
+  constexpr int kV = D / 32, kAhead = 4, kRows = kSpMergeWarps / WPR;
+  __shared__ float part[WPR > 1 ? kRows : 1][WPR][D + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rw = warp / WPR, w = warp % WPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + rw;
+  const bool real = row < static_cast<int64_t>(p.num_seqs) * p.num_heads;
+  const int b = real ? static_cast<int>(row / p.num_heads) : 0;
+  const int h = real ? static_cast<int>(row - static_cast<int64_t>(b) * p.num_heads) : 0;
   const int kvh = h / p.group, g = h - kvh * p.group;
-  const int2 sq = p.seq[b];  // tokens from the prefix unit, length
-  T* o = static_cast<T*>(p.out) + row * D + lane * kV;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t at = static_cast<int64_t>(b) * p.num_kv_heads + kvh;
-  int4 ps = make_int4(0, -1, 0, 0), rs = make_int4(0, -1, 0, 0);
-  auto span = [&](const int4* s) {  // CTAs in range whatever a call that timed out left there
-    int4 v = s[at];
+  const int2 sq = p.seq[b];  // tokens from the prefix unit, length
+  int4 ps = p.pre_span[at], rs = p.rest_span[at];
+  auto clamped = [&](int4 v) {  // CTAs in range whatever a call that timed out left there
     v.x = max(0, min(v.x, p.num_ctas - 1));
     v.y = max(v.x, min(v.y, p.num_ctas - 1));
     v.z = max(0, min(v.z, kSpRows - p.group));
     return v;
   };
-  if (sq.x > 0) ps = span(p.pre_span);
-  if (sq.y > sq.x) rs = span(p.rest_span);
-  const int np = ps.y - ps.x + 1, nr = rs.y - rs.x + 1, n = np + nr;
-  if (sq.x == 0 && nr == 1) return;  // written by the first kernel
-  // piece i's row among the workspace's rows, and which array it is in
-  auto place = [&](int i, bool& cut) -> int64_t {
-    const bool pre = i < np;
-    const int4 s = pre ? ps : rs;
-    const int k = pre ? i : i - np;
-    cut = s.x != s.y;
-    return cut ? (static_cast<int64_t>(s.x + k) * 2 + (k == 0 ? 1 : 0)) * kSpRows + s.z + g
-               : row + (pre ? 0 : static_cast<int64_t>(p.num_seqs) * p.num_heads);
-  };
+  ps = sq.x > 0 ? clamped(ps) : make_int4(0, -1, 0, 0);
+  rs = sq.y > sq.x ? clamped(rs) : make_int4(0, -1, 0, 0);
+  const int np = ps.y - ps.x + 1, nr = rs.y - rs.x + 1;
+  const bool skip = !real || (sq.x == 0 && nr == 1);  // written by the first kernel
+  const int n = skip ? 0 : np + nr;
   float m = -INFINITY, den = 0.f, acc[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) acc[v] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float mi = -INFINITY, li = 0.f;
-    int64_t pr = 0;
-    bool cut = false;
-    if (i0 + lane < n) {
-      pr = place(i0 + lane, cut);
-      const float2 ml = *reinterpret_cast<const float2*>((cut ? p.cut_ml : p.unit_ml) + pr * 2);
-      li = ml.y;
-      if (li > 0.f) mi = ml.x;  // a piece with no weight says nothing
-    }
-    float mx = mi;
+  for (int i0 = w; i0 < n; i0 += WPR * kAhead) {
+    float2 ml[kAhead];
+    float y[kAhead][kV];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    mx = fmaxf(mx, m);
-    if (mx == -INFINITY) continue;
-    const float old = fast_exp2(m - mx), w = mi == -INFINITY ? 0.f : fast_exp2(mi - mx);
-    float sum = w * li;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    den = den * old + sum;
-    m = mx;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] *= old;
-    const int cnt = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const int64_t ri = __shfl_sync(0xffffffffu, pr, i);
-      const bool ci = __shfl_sync(0xffffffffu, cut ? 1 : 0, i) != 0;
-      const float* src = (ci ? p.cut_o : p.unit_o) + ri * D + lane * kV;
-      float y[kV];
-      if constexpr (kV == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
-      else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
-      if (wi > 0.f) {
-#pragma unroll
-        for (int v = 0; v < kV; ++v) acc[v] += wi * y[v];
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * WPR;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (i < n) {
+        // piece i: row of the whole units' array, or of a CTA's cut pieces
+        // (the first CTA's is its last piece, the others' their first)
+        const bool pre = i < np;
+        const int4 s = pre ? ps : rs;
+        const int c = pre ? i : i - np;
+        const bool cut = s.x != s.y;
+        const int64_t pr = cut ? (static_cast<int64_t>(s.x + c) * 2 + (c == 0 ? 1 : 0)) * kSpRows + s.z + g
+                               : row + (pre ? 0 : static_cast<int64_t>(p.num_seqs) * p.num_heads);
+        ml[k] = *reinterpret_cast<const float2*>((cut ? p.cut_ml : p.unit_ml) + pr * 2);
+        const float* src = (cut ? p.cut_o : p.unit_o) + pr * D + lane * kV;
+        if constexpr (kV == 4) *reinterpret_cast<float4*>(y[k]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(y[k]) = *reinterpret_cast<const float2*>(src);
       }
     }
-  }
-  const float inv = den > 0.f ? __fdiv_rn(1.f, den) : 0.f;
 #pragma unroll
-  for (int v = 0; v < kV; v += 2)
-    *reinterpret_cast<uint32_t*>(o + v) = Mma<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+    for (int k = 0; k < kAhead; ++k) {
+      if (!(ml[k].y > 0.f)) continue;  // no such piece, or one without weight
+      const float mx = fmaxf(m, ml[k].x);
+      const float old = fast_exp2(m - mx), wt = fast_exp2(ml[k].x - mx);
+      m = mx;
+      den = den * old + wt * ml[k].y;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[v] = acc[v] * old + wt * y[k][v];
+    }
+  }
+  if constexpr (WPR > 1) {
+    if (w > 0) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) part[rw][w][lane * kV + v] = acc[v];
+      if (lane == 0) {
+        part[rw][w][D] = m;
+        part[rw][w][D + 1] = den;
+      }
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      const float mk = part[rw][k][D], dk = part[rw][k][D + 1];
+      if (!(dk > 0.f)) continue;
+      const float mx = fmaxf(m, mk), old = fast_exp2(m - mx), wt = fast_exp2(mk - mx);
+      m = mx;
+      den = den * old + wt * dk;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[v] = acc[v] * old + wt * part[rw][k][lane * kV + v];
+    }
+  }
+  if (skip) return;
+  T* o = static_cast<T*>(p.out) + row * D + lane * kV;
+  const float inv = den > 0.f ? __fdiv_rn(1.f, den) : 0.f;
+  if constexpr (kV == 4)
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(Mma<T>::pack(acc[0] * inv, acc[1] * inv), Mma<T>::pack(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(o) = Mma<T>::pack(acc[0] * inv, acc[1] * inv);
 }
 
 // ------------------------------------------------------------------- host
@@ -793,6 +861,21 @@ SpWorkspace sp_workspace(int B, int Hq, int Hkv, int D, int ctas) {
 // Shared memory per CTA with two CTAs on an SM, and with one.
 constexpr int kSpSmemTwo = 112 * 1024, kSpSmemOne = 226 * 1024;
 
+template <typename T, int D, int WPR>
+cudaError_t launch_merge(const SpParams& p, int64_t rows, cudaStream_t st) {
+  constexpr int kRows = kSpMergeWarps / WPR;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kRows - 1) / kRows));
+  cfg.blockDim = dim3(kSpMergeWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<T, D, WPR>, p);
+}
+
 template <typename T, int D>
 cudaError_t launch_shared(SpParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t st) {
   using Lay = SpLayout<D>;
@@ -816,10 +899,11 @@ cudaError_t launch_shared(SpParams& p, const CUtensorMap& mk, const CUtensorMap&
   kern<<<p.num_ctas, kSpThreads, smem, st>>>(p, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // few rows: up to eight warps join one
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_heads;
-  shared_merge_kernel<T, D><<<static_cast<unsigned>((rows + kSpMergeWarps - 1) / kSpMergeWarps), kSpMergeWarps * 32, 0,
-                              st>>>(p);
-  return cudaGetLastError();
+  if (rows * 8 <= static_cast<int64_t>(sms) * 64) return launch_merge<T, D, 8>(p, rows, st);
+  if (rows * 2 <= static_cast<int64_t>(sms) * 64) return launch_merge<T, D, 2>(p, rows, st);
+  return launch_merge<T, D, 1>(p, rows, st);
 }
 
 }  // namespace
