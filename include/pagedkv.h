@@ -598,9 +598,9 @@ int paged_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_heads, int3
  *     the call; calls that share one (captured graphs too) must be ordered.
  * The remaining arguments, their rules and errors are those of
  * paged_decode_attention.  fp16 and bf16 with head_dim 64 or 128, block_size
- * 16, 32, 64 or 128, at most 128 query heads per kv head and 4096 sequences
- * run on the 5th-generation tensor cores (two launches); every other shape
- * is one paged_decode_attention call.  fp32 accumulation and online softmax,
+ * 16, 32, 64 or 128, at most 16 query heads per kv head and 4096 sequences
+ * share prefixes (two launches, the prefixes on the 5th-generation tensor
+ * cores); every other shape is one paged_decode_attention call.  fp32 accumulation and online softmax,
  * one rounding to dtype. */
 int paged_decode_attention_shared_prefix(void* out, const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, const int32_t* seq_lens,

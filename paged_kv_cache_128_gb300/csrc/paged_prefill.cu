@@ -62,17 +62,6 @@ __device__ __forceinline__ uint32_t pf_off(int key, int d) {
                                (d & 7) * 2);
 }
 
-// 16-byte async copy; with valid == false nothing is read and zeros land.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const PrefillParams p) {
   using M = Mma<T>;

@@ -12,27 +12,30 @@
 // a range of keys of one kv head:
 //   prefix unit (group, row tile, kv head): the G query heads of up to
 //     128 / G sequences of the group against keys 0 .. P_g - 1, which are
-//     read once for all of them;
-//   rest unit (sequence, kv head): G rows against keys P_g .. L_b - 1.
+//     read once for all of them: matrix products with 128 rows;
+//   rest unit (sequence, kv head): G rows against keys P_g .. L_b - 1: the
+//     few rows of ordinary decode attention.
 //
 // What bounds it: every group's prefix and every sequence's rest are read
 // once (a second row tile of a group finds the prefix in L2), 4 D flops per
 // query row and key; memory until about 280 query rows share each key, then
 // the tensor cores.
 //
-// Partition.  The units in order (groups, then sequences; kv head; row tile)
-// lie on a line, each a fixed charge followed by its 64-key tiles.  The line
-// is cut into equal lengths, one per CTA (two persistent CTAs per SM), so the
-// load is even whatever the mix of group sizes and lengths, and a unit is cut
-// only where a CTA's share ends.  A rest unit of a sequence without prefix
-// that falls whole into one CTA is written to `out`; every other piece writes
-// (o, m, l) in float32 to the workspace, and shared_merge_kernel joins a
-// row's pieces, in their order along the line, so results do not depend on
-// timing.  Every CTA rebuilds the line from group_start, prefix_lens and
-// seq_lens in shared memory; nothing in the workspace outlives the call.
+// Partition.  The prefix units in order (group; kv head; row tile) lie on one
+// line, each a fixed charge followed by its 64-key tiles, the rest units
+// (sequence; kv head) on another, each a charge and its 16-token tiles.  The
+// first CTAs of one wave (two per SM) share the first line, the warps of the
+// others the second one, in equal lengths, and the number of CTAs on each
+// side follows the lines' weights; so a unit is cut only where a share ends.
+// A rest unit of a sequence without prefix that falls whole into one warp's
+// share is written to `out`; every other piece writes (o, m, l) in float32 to
+// the workspace, and shared_merge_kernel joins a row's pieces in their order
+// along the lines, so results do not depend on timing.  Every CTA rebuilds
+// the lines from group_start, prefix_lens and seq_lens in shared memory;
+// nothing in the workspace outlives the call.
 //
-// Warps of a CTA (the tcgen05 pipeline of the chunked prefill, at 64 keys a
-// tile and with two score buffers):
+// A prefix CTA is the tcgen05 pipeline of the chunked prefill, at 64 keys a
+// tile and with two score buffers:
 //   warp 5: TMA: K and V tiles through the block table into one ring of
 //     stages, K_0 V_0 K_1 V_1 ..., across unit boundaries;
 //   warp 4: one lane issues the MMAs, M 128: S = Q K^T (N 64) into one of two
@@ -43,9 +46,12 @@
 //     maximum passes it by 2^8; warps without a row of the unit skip the
 //     arithmetic.  They also lay a unit's Q into shared memory (any G: the
 //     rows are gathered) and write its results.
-// Rest units fill only G of the 128 rows; a 64-key tile's MMAs then take about
-// 0.27 us of an SM's tensor pipe against 0.73 us of its share of the memory
-// rate (D 128), so the idle rows cost no time.
+// In a rest CTA each of warps 0-3 works by itself: its own ring of 16-token
+// tiles, its own copies, the decode kernels' mma.sync step (tokens in M, heads
+// in N) and its unit's whole softmax state in registers, so that a unit of a
+// few tokens costs no exchange between warps.  (Rest units through the
+// tcgen05 pipeline cost 3.3 us each at one 64-key tile, with 5 of 128 rows
+// in use.)
 
 #include <cudaTypedefs.h>
 
@@ -55,13 +61,14 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "decode_tile.cuh"
 #include "tcgen05.cuh"
 
 namespace pagedkv {
 namespace {
 
-constexpr int kSpRows = 128;   // MMA M: query rows of a unit
-constexpr int kSpKeys = 64;    // keys per tile: N of S, K of P V
+constexpr int kSpRows = 128;   // MMA M: query rows of a prefix unit
+constexpr int kSpKeys = 64;    // keys per prefix tile: N of S, K of P V
 constexpr int kSpSoftWarps = 4;
 constexpr int kSpMmaWarp = kSpSoftWarps, kSpTmaWarp = kSpSoftWarps + 1;
 constexpr int kSpThreads = 32 * (kSpSoftWarps + 2);
@@ -72,9 +79,13 @@ constexpr uint32_t kSpCols = 256;  // S buffers at columns 0 and 64 (P over the 
 // behind at most.
 constexpr int kSpMinStages = 3, kSpMaxStages = 8;
 constexpr int kSpMaxSeqs = 4096;
-// Tiles' worth of time that a unit costs beyond its tiles (its Q, the
-// pipeline's turn-round, its partial result).
-constexpr int kSpUnitCost = 3;
+constexpr int kSpMaxGroup = 16;  // query heads per kv head: rows of a rest unit (two n8 blocks)
+constexpr int kSpTok = 16;       // tokens per rest tile
+constexpr int kSpMaxRest = 6;    // stages of a warp's ring of rest tiles
+// Charges, in tiles of the unit's line, for what a unit costs beyond its
+// tiles, and the weight of a prefix tile against a rest tile.
+constexpr int kSpPrefixCost = 4, kSpRestCost = 2;
+constexpr int kSpPrefixWeight = 4, kSpRestWeight = 1;
 
 struct SpParams {
   void* out;
@@ -86,16 +97,18 @@ struct SpParams {
   int32_t num_seqs, num_groups, num_heads, num_kv_heads, group, block_size, tile_seqs;
   int64_t num_blocks;
   int32_t max_blocks_per_seq;
-  int32_t stages;
+  int32_t stages, rest_stages;
   float scale_log2;  // scale * log2(e)
   int32_t num_ctas;
   // workspace
-  float* unit_o;    // [2][B][Hq][D] whole units: prefix, rest
-  float* unit_ml;   // [2][B][Hq][2] (reference, sum)
-  float* cut_o;     // [CTA][2][kSpRows][D] pieces of units cut by a CTA's share: its first, its last
-  float* cut_ml;    // [CTA][2][kSpRows][2]
-  int4* pre_span;   // [B][Hkv] first and last CTA of the sequence's prefix unit, its first row there
-  int4* rest_span;  // [B][Hkv] the same of its rest unit
+  float* unit_o;   // [2][B][Hq][D] whole units: prefix, rest
+  float* unit_ml;  // [2][B][Hq][2] (reference, sum)
+  float* pre_o;    // [CTA][2][kSpRows][D] pieces of prefix units cut by a CTA's share: its first, its last
+  float* pre_ml;   // [CTA][2][kSpRows][2]
+  float* rest_o;   // [warp][2][G][D] the same of rest units and a warp's share
+  float* rest_ml;  // [warp][2][G][2]
+  int4* pre_span;   // [B][Hkv] first and last share of the sequence's prefix unit, its first row there
+  int4* rest_span;  // [B][Hkv] first and last share of its rest unit
   int2* seq;        // [B] (tokens taken from the prefix unit, length)
 };
 
@@ -106,104 +119,133 @@ struct SpLayout {
   static constexpr int kQ = kSlabs * kQSlab;
   static constexpr int kSlab = kSpKeys * 128;   // 64 dims of a tile's 64 keys
   static constexpr int kTile = kSlabs * kSlab;
-  static constexpr int kBars = 256;
+  static constexpr int kRestTile = kSpTok * D * 2;  // K or V of a rest tile
+  static constexpr int kBars = 8 * (2 * kSpMaxStages + 8 + kSpSoftWarps * kSpMaxRest) + 64;
+  // a rest CTA uses the bytes of Q and the stages for its warps' rings
+  static int rest_stages(int stages) {
+    return std::min(kSpMaxRest, (kQ + stages * kTile) / (kSpSoftWarps * 2 * kRestTile));
+  }
   static int bytes(int stages, int num_seqs, int num_groups) {
-    return 1024 + kQ + stages * kTile + kBars + 4 * (3 * num_seqs + 3 * num_groups + 2);
+    return 1024 + kQ + stages * kTile + kBars + 4 * (3 * num_seqs + 3 * num_groups + 3);
   }
 };
 
-// The line of units, in shared memory.
+// The lines of units, in shared memory.
 struct SpLine {
-  int* cum;    // [groups + seqs + 1] cost per kv head before each entity (a group's prefix units, a sequence's rest)
-  int* start;  // [groups + 1] group_start
+  int* pre;     // [groups + 1] prefix line: cost per kv head before each group
+  int* rest;    // [seqs + 1] rest line: cost per kv head before each sequence
+  int* start;   // [groups + 1] group_start
   int* prefix;  // [groups] tokens of the group's prefix that are shared (whole blocks)
-  int* first;  // [seqs] tokens the sequence takes from its group's prefix unit
-  int* len;    // [seqs]
+  int* first;   // [seqs] tokens the sequence takes from its group's prefix unit
+  int* len;     // [seqs]
 };
 
-struct SpUnit {
-  int b0, rows;    // first sequence, query rows
-  int kvh;
-  int key0, key1;  // keys
-  int t0, t1, T;   // tiles of it in this CTA, its tiles in all
-  int64_t base;    // its place on the line
-  bool prefix;
-};
+// The last entity of a line (cost prefix sums cum[0..n]) that begins at or
+// before place x < hkv cum[n]; it is not empty.
+__device__ __forceinline__ int sp_entity(const int* cum, int n, int hkv, int64_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(hkv) * cum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
 
-// Walks the units of CTA pid's share in order.  Every role of the CTA walks
-// for itself.
-struct SpWalk {
+// Of P shares [s W / P, (s + 1) W / P), the one that holds place t.
+__device__ __forceinline__ int sp_share_of(int64_t t, int64_t W, int P) {
+  return static_cast<int>(((t + 1) * P + W - 1) / W - 1);
+}
+
+// Prefix units of a share of the prefix line, in order.
+struct SpPrefixWalk {
   const SpParams& p;
   const SpLine& ln;
-  int64_t x, x1, base;
-  int e, u, units, cs, rt_n, n;
+  int64_t x, x1, base;  // place reached, the share's end, the unit's place
+  int e, u, cs, row_tiles, n;  // group, unit in it, a unit's cost, row tiles, sequences
+  // the unit
+  int b0, rows, kvh, keys, t0, t1, T;
+  int64_t at;
 
-  __device__ __forceinline__ SpWalk(const SpParams& p_, const SpLine& ln_, int64_t x0_, int64_t x1_)
-      : p(p_), ln(ln_), x(x0_), x1(x1_), base(0), e(0), u(0), units(0), cs(1), rt_n(1), n(1) {
-    int lo = 0, hi = p.num_groups + p.num_seqs - 1;  // the last entity that begins at or before x: it is not empty
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(p.num_kv_heads) * ln.cum[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    enter(lo);
+  __device__ __forceinline__ SpPrefixWalk(const SpParams& p_, const SpLine& ln_, int64_t x0, int64_t x1_)
+      : p(p_), ln(ln_), x(x0), x1(x1_) {
+    enter(sp_entity(ln.pre, p.num_groups, p.num_kv_heads, x));
     u = static_cast<int>((x - base) / cs);
     base += static_cast<int64_t>(u) * cs;
   }
-  __device__ __forceinline__ void enter(int e_) {
-    e = e_;
+  __device__ __forceinline__ void enter(int g) {
+    e = g;
     u = 0;
-    const int per_head = ln.cum[e + 1] - ln.cum[e];
-    rt_n = 1;
-    n = 1;
-    if (e < p.num_groups) {
-      n = ln.start[e + 1] - ln.start[e];
-      rt_n = (n + p.tile_seqs - 1) / p.tile_seqs;
-    }
-    cs = per_head / rt_n;
-    units = p.num_kv_heads * rt_n;
-    base = static_cast<int64_t>(p.num_kv_heads) * ln.cum[e];
+    n = ln.start[g + 1] - ln.start[g];
+    row_tiles = (n + p.tile_seqs - 1) / p.tile_seqs;
+    cs = (ln.pre[g + 1] - ln.pre[g]) / row_tiles;
+    base = static_cast<int64_t>(p.num_kv_heads) * ln.pre[g];
   }
-  // The next unit with a tile in the share, or false.
-  __device__ __forceinline__ bool next(SpUnit& s) {
+  // To the next unit with a tile in the share; false when there is none.
+  __device__ __forceinline__ bool next() {
     while (x < x1) {
-      s.T = cs - kSpUnitCost;
-      s.t0 = static_cast<int>(max(static_cast<int64_t>(0), x - base - kSpUnitCost));
-      s.t1 = static_cast<int>(min(static_cast<int64_t>(s.T), x1 - base - kSpUnitCost));
-      s.base = base;
-      s.kvh = u / rt_n;
-      if (e < p.num_groups) {
-        const int rt = u - s.kvh * rt_n;
-        s.prefix = true;
-        s.b0 = ln.start[e] + rt * p.tile_seqs;
-        s.rows = min(p.tile_seqs, n - rt * p.tile_seqs) * p.group;
-        s.key0 = 0;
-        s.key1 = ln.prefix[e];
-      } else {
-        s.prefix = false;
-        s.b0 = e - p.num_groups;
-        s.rows = p.group;
-        s.key0 = ln.first[s.b0];
-        s.key1 = ln.len[s.b0];
-      }
+      T = cs - kSpPrefixCost;
+      t0 = static_cast<int>(max(static_cast<int64_t>(0), x - base - kSpPrefixCost));
+      t1 = static_cast<int>(min(static_cast<int64_t>(T), x1 - base - kSpPrefixCost));
+      at = base;
+      kvh = u / row_tiles;
+      const int rt = u - kvh * row_tiles;
+      b0 = ln.start[e] + rt * p.tile_seqs;
+      rows = min(p.tile_seqs, n - rt * p.tile_seqs) * p.group;
+      keys = ln.prefix[e];
       base += cs;
       x = base;
-      if (++u == units && x < x1) {
-        int en = e + 1;
-        const int E = p.num_groups + p.num_seqs;
-        while (en < E && ln.cum[en + 1] == ln.cum[en]) ++en;
-        if (en < E) enter(en);
-        else x1 = x;
+      if (++u == p.num_kv_heads * row_tiles && x < x1) {
+        int g = e + 1;
+        while (ln.pre[g + 1] == ln.pre[g]) ++g;  // x < x1: a group with units follows
+        enter(g);
       }
-      if (s.t1 > s.t0) return true;
+      if (t1 > t0) return true;
     }
     return false;
   }
 };
 
-// The CTA whose share [c W / P, (c + 1) W / P) holds place t.
-__device__ __forceinline__ int sp_cta_of(int64_t t, int64_t W, int P) {
-  return static_cast<int>(((t + 1) * P + W - 1) / W - 1);
-}
+// Tiles of a share of the rest line, in order: tile t of unit (b, kvh).
+struct SpRestWalk {
+  int b, kvh, t, t0, t1, T, first, len;
+  int64_t base, x1;
+
+  __device__ __forceinline__ void enter(const SpLine& ln, int b_) {
+    b = b_;
+    T = ln.rest[b + 1] - ln.rest[b] - kSpRestCost;
+    first = ln.first[b];
+    len = ln.len[b];
+  }
+  __device__ __forceinline__ bool span(int64_t x) {  // tiles of the unit from place x on
+    t0 = static_cast<int>(max(static_cast<int64_t>(0), x - base - kSpRestCost));
+    t1 = static_cast<int>(min(static_cast<int64_t>(T), x1 - base - kSpRestCost));
+    t = t0;
+    return t0 < t1;
+  }
+  __device__ __forceinline__ bool begin(const SpParams& p, const SpLine& ln, int64_t x0, int64_t x1_) {
+    x1 = x1_;
+    if (x0 >= x1) return false;
+    enter(ln, sp_entity(ln.rest, p.num_seqs, p.num_kv_heads, x0));
+    base = static_cast<int64_t>(p.num_kv_heads) * ln.rest[b];
+    kvh = static_cast<int>((x0 - base) / (T + kSpRestCost));
+    base += static_cast<int64_t>(kvh) * (T + kSpRestCost);
+    return span(x0) || next_unit(p, ln);
+  }
+  __device__ __forceinline__ bool next_unit(const SpParams& p, const SpLine& ln) {
+    base += T + kSpRestCost;
+    if (base + kSpRestCost >= x1) return false;  // its first tile is another share's
+    if (++kvh == p.num_kv_heads) {
+      kvh = 0;
+      int n = b + 1;
+      while (ln.rest[n + 1] == ln.rest[n]) ++n;  // base < x1: a sequence with a rest follows
+      enter(ln, n);
+    }
+    return span(base);
+  }
+  __device__ __forceinline__ bool next(const SpParams& p, const SpLine& ln) {
+    return ++t < t1 || next_unit(p, ln);
+  }
+};
 
 // 32-byte store: a thread's piece of its row is a whole sector.
 __device__ __forceinline__ void st_global_32b(float* p, const uint32_t* v) {
@@ -212,98 +254,531 @@ __device__ __forceinline__ void st_global_32b(float* p, const uint32_t* v) {
                : "memory");
 }
 
-__device__ __forceinline__ int sp_len(const SpParams& p, int b) {
-  int L = __ldg(p.seq_lens + b);
-  const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
-  if (L < 0 || L > cap) {
-    record_error(KV_ERR_DEVICE_BOUNDS);
-    L = L < 0 ? 0 : static_cast<int>(cap);
+// One warp's share [x0, x1) of the rest line; `share` is its index, P the
+// number of shares.
+template <typename T, int D, int NG>
+__device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
+                                          const CUtensorMap& tmV, uint8_t* ring, uint64_t* full, int64_t W, int P,
+                                          int share, int lane) {
+  constexpr int kRestTile = SpLayout<D>::kRestTile;
+  const int G = p.group, bs = p.block_size, nst = p.rest_stages;
+  const int64_t x0 = share * W / P, x1 = (share + 1) * W / P;
+  SpRestWalk iw, cw;  // where the copies are, where the arithmetic is
+  bool imore = iw.begin(p, ln, x0, x1);
+  bool more = cw.begin(p, ln, x0, x1);
+  // Table entries are fetched 32 at a time, one per lane, and the chunk the
+  // walk is likely to need next is fetched along.
+  auto fetch = [&](int b, int chunk) -> int {
+    const int e = (chunk << 5) + lane;
+    return e < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq + e) : 0;
+  };
+  int have_b = -1, have_c = -1, mine = 0, next_b = -1, next_c = -1, nxt = 0;
+  int issued = 0, ist = 0;
+  auto issue = [&]() {  // the copies of the issue walk's tile into stage ist
+    const int tok = iw.first + iw.t * kSpTok, blk = tok / bs, off = tok - blk * bs;
+    const int c = blk >> 5;
+    if (iw.b != have_b || c != have_c) {
+      mine = iw.b == next_b && c == next_c ? nxt : fetch(iw.b, c);
+      have_b = iw.b;
+      have_c = c;
+      next_b = iw.b;
+      next_c = c + 1;
+      if ((next_c << 5) * bs >= iw.len) {  // the sequence's last chunk
+        next_b = iw.b + 1;
+        next_c = next_b < p.num_seqs ? ln.first[next_b] / bs >> 5 : 0;
+      }
+      if (next_b < p.num_seqs) nxt = fetch(next_b, next_c);
+    }
+    int pb = __shfl_sync(0xffffffffu, mine, blk & 31);
+    if (lane == 0) {
+      if (pb < 0 || pb >= p.num_blocks) {
+        record_error(KV_ERR_DEVICE_BOUNDS);
+        pb = 0;
+      }
+      uint8_t* dst = ring + ist * 2 * kRestTile;
+      mbar_arrive_expect_tx(full + ist, 2 * kRestTile);
+      tma_load_4d(dst, &tmK, full + ist, 0, pb * bs + off, 0, iw.kvh);
+      tma_load_4d(dst + kRestTile, &tmV, full + ist, 0, pb * bs + off, 0, iw.kvh);
+    }
+    ++issued;
+    if (++ist == nst) ist = 0;
+    imore = iw.next(p, ln);
+  };
+  auto q_of = [&](const SpRestWalk& w) {
+    return static_cast<const T*>(p.q) + (static_cast<int64_t>(w.b) * p.num_heads + w.kvh * G) * D;
+  };
+  WarpState<D, NG> st;
+  // the next unit's Q is fetched one unit ahead where the registers allow
+  constexpr bool kAheadQ = (D / 16) * NG * 2 <= 16;
+  uint32_t qn[D / 16][NG][2];
+  auto fetch_next_q = [&]() {
+    if constexpr (kAheadQ) {
+      SpRestWalk w = cw;
+      if (w.next_unit(p, ln)) load_q_frags<T, D, NG>(qn, q_of(w), G, lane);
+    }
+  };
+  for (int i = 0; i < nst && imore; ++i) issue();
+  if (more) {
+    load_q<T, D, NG>(st, q_of(cw), G, lane);
+    fetch_next_q();
   }
-  return L;
+  reset_state(st);
+  int cst = 0, phase = 0, ok = 1, done = 0;
+  while (more && ok) {
+    if (lane == 0) ok = mbar_wait_bounded(full + cst, phase);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    __syncwarp();
+    uint8_t* kt = ring + cst * 2 * kRestTile;
+    consume_tile<T, D, kSpTok, NG>(st, kt, kt + kRestTile, cw.first + cw.t * kSpTok, cw.len, p.scale_log2, lane);
+    __syncwarp();
+    ++done;
+    if (imore) issue();  // into the stage just read
+    if (++cst == nst) {
+      cst = 0;
+      phase ^= 1;
+    }
+    if (cw.t + 1 < cw.t1) {
+      ++cw.t;
+      continue;
+    }
+    // ---- the share's piece of the unit is complete
+    const bool whole = cw.t0 == 0 && cw.t1 == cw.T, direct = whole && cw.first == 0;
+    const int64_t orow = static_cast<int64_t>(cw.b) * p.num_heads + cw.kvh * G;
+    const int64_t urow = orow + static_cast<int64_t>(p.num_seqs) * p.num_heads;
+    const int64_t crow = (static_cast<int64_t>(share) * 2 + (cw.t0 == 0 ? 1 : 0)) * G;
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) st.l[ng][c] += __shfl_xor_sync(0xffffffffu, st.l[ng][c], o);
+    float* po = whole ? p.unit_o + urow * D : p.rest_o + crow * D;
+    float* pml = whole ? p.unit_ml + urow * 2 : p.rest_ml + crow * 2;
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int g = ng * 8 + (lane & 3) * 2 + c;
+        if (g >= G) continue;
+        if (direct) {
+          const float inv = st.l[ng][c] > 0.f ? __fdiv_rn(1.f, st.l[ng][c]) : 0.f;
+          T* o = static_cast<T*>(p.out) + (orow + g) * D + (lane >> 2);
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[mt * 16] = DType<T>::from_float(st.acc[mt][ng][c] * inv);
+            o[mt * 16 + 8] = DType<T>::from_float(st.acc[mt][ng][c + 2] * inv);
+          }
+        } else {
+          float* o = po + static_cast<int64_t>(g) * D + (lane >> 2);
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[mt * 16] = st.acc[mt][ng][c];
+            o[mt * 16 + 8] = st.acc[mt][ng][c + 2];
+          }
+          if (lane < 4) *reinterpret_cast<float2*>(pml + g * 2) = make_float2(st.m[ng][c], st.l[ng][c]);
+        }
+      }
+    if (cw.t0 == 0 && lane == 0) {  // the unit's first share says where its pieces lie
+      const int last = whole ? share : sp_share_of(cw.base + kSpRestCost + cw.T - 1, W, P);
+      p.rest_span[static_cast<int64_t>(cw.b) * p.num_kv_heads + cw.kvh] = make_int4(share, last, 0, 0);
+    }
+    more = cw.next_unit(p, ln);
+    if (more) {
+      if constexpr (kAheadQ) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng) {
+            st.qf[kk][ng][0] = qn[kk][ng][0];
+            st.qf[kk][ng][1] = qn[kk][ng][1];
+          }
+        fetch_next_q();
+      } else {
+        load_q<T, D, NG>(st, q_of(cw), G, lane);
+      }
+      reset_state(st);
+    }
+  }
+  if (!ok && lane == 0)  // a wait ran out: let the copies in flight land (bounded) before the CTA ends
+    for (int i = done + 1; i < issued; ++i) mbar_wait_bounded(full + i % nst, (i / nst) & 1);
 }
 
-// Registers: two CTAs of six warps, at most 168 a thread (as the prefill).
+// A CTA's share [x0, x1) of the prefix line.
 template <typename T, int D>
-__global__ void __launch_bounds__(kSpThreads, 2)
-    shared_prefix_kernel(const SpParams p, const __grid_constant__ CUtensorMap tmK,
-                         const __grid_constant__ CUtensorMap tmV) {
+__device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
+                                           const CUtensorMap& tmV, uint8_t* sm, uint64_t* bars, uint32_t tmem,
+                                           int64_t W, int P, int share) {
   using Lay = SpLayout<D>;
   constexpr int kSlabs = Lay::kSlabs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ uint8_t sp_smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sp_smem_raw) + 1023) & ~uintptr_t(1023));
-  const int nst = p.stages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nst = p.stages, bs = p.block_size;
   uint8_t* ring = sm + Lay::kQ;
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(ring + nst * Lay::kTile);  // [stage] tile landed
+  uint64_t* bar_full = bars;                      // [stage] tile landed
   uint64_t* bar_empty = bar_full + kSpMaxStages;  // [stage] its MMAs done
   uint64_t* bar_q = bar_empty + kSpMaxStages;     // a unit's Q laid down (every softmax thread)
   uint64_t* bar_o = bar_q + 1;                    // a unit's O read (every softmax thread)
   uint64_t* bar_s = bar_o + 1;                    // [2] S written
   uint64_t* bar_p = bar_s + 2;                    // [2] P written (every softmax thread)
   uint64_t* bar_pv = bar_p + 2;                   // [2] P V done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_pv + 2);
-  const int B = p.num_seqs, NG = p.num_groups, E = NG + B;
+  SpPrefixWalk w(p, ln, share * W / P, (share + 1) * W / P);
+  if (warp == kSpTmaWarp) {
+    // ---- K and V tiles, one box of up to 64 rows per (block, 64-dim slab)
+    const int rpc = min(bs, kSpKeys);  // rows of a box
+    const int ci = lane / kSlabs, slab = lane % kSlabs;
+    // table entry of this lane's box of tile t and the box's offset in the
+    // block (-1: no box); the entry is looked at only when the box is copied
+    auto entry = [&](int t, int& off) -> int {
+      const int tok = t * kSpKeys + ci * rpc;
+      off = -1;
+      if (ci * rpc >= kSpKeys || tok >= w.keys) return 0;
+      const int blk = tok / bs;
+      off = tok - blk * bs;
+      return __ldg(p.block_tables + static_cast<int64_t>(w.b0) * p.max_blocks_per_seq + blk);
+    };
+    int t = 0;
+    auto step = [&]() -> bool {
+      if (++t < w.t1) return true;
+      if (!w.next()) return false;
+      t = w.t0;
+      return true;
+    };
+    // the table entries of two tiles are in flight ahead of their copies
+    int ok = 1, i = 0, off = -1, off1 = -1, off2 = -1;
+    bool more = w.next();
+    t = w.t0;
+    int pb = more ? entry(t, off) : 0, kvh = w.kvh;
+    bool more1 = more && step();
+    int pb1 = more1 ? entry(t, off1) : 0, kvh1 = w.kvh;
+    while (more && ok) {
+      const bool more2 = more1 && step();
+      off2 = -1;
+      const int pb2 = more2 ? entry(t, off2) : 0, kvh2 = w.kvh;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, off >= 0));
+      if (off >= 0 && (pb < 0 || pb >= p.num_blocks)) {
+        record_error(KV_ERR_DEVICE_BOUNDS);
+        pb = 0;
+      }
+      const int row = pb * bs + off;
+      for (int v = 0; v < 2 && ok; ++v, ++i) {
+        const int st = i % nst;
+        if (lane == 0) {
+          if (i >= nst) ok = mbar_wait_bounded(bar_empty + st, (i / nst - 1) & 1);
+          if (ok) mbar_arrive_expect_tx(bar_full + st, static_cast<uint32_t>(boxes * rpc * 128));
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok && off >= 0)
+          tma_load_3d(ring + st * Lay::kTile + slab * Lay::kSlab + ci * rpc * 128, v ? &tmV : &tmK, bar_full + st,
+                      slab * 64, kvh, row);
+      }
+      pb = pb1, off = off1, kvh = kvh1, more = more1;
+      pb1 = pb2, off1 = off2, kvh1 = kvh2, more1 = more2;
+    }
+    // every stage's last MMAs have completed: no copy or commit in flight at exit
+    if (lane == 0 && ok)
+      for (int k = max(0, i - nst); k < i; ++k) mbar_wait_bounded(bar_empty + k % nst, (k / nst) & 1);
+  } else if (warp == kSpMmaWarp) {
+    if (lane == 0) {
+      // ---- MMA issue
+      constexpr uint32_t idS = tc::idesc_f16(kBf16, kSpRows, kSpKeys, false);
+      constexpr uint32_t idPV = tc::idesc_f16(kBf16, kSpRows, D, true);
+      const uint32_t aQ = smem_u32(sm), ring_a = smem_u32(ring);
+      // S of tile j (first: of unit number un) once its K, the unit's Q
+      // and its buffer (P V of tile j - 2 done) are ready
+      auto issue_s = [&](int j, bool first, int un) -> bool {
+        const int i = 2 * j, st = i % nst;
+        if (first && !mbar_wait_bounded(bar_q, un & 1)) return false;
+        if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
+        if (j >= 2 && !mbar_wait_bounded(bar_pv + (j & 1), ((j >> 1) - 1) & 1)) return false;
+        tc::fence_after();
+        const uint32_t kb = ring_a + st * Lay::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_f16(tmem + (j & 1) * 64, tc::sdesc_sw128(aQ + (kk >> 2) * Lay::kQSlab + (kk & 3) * 32, 16, 1024),
+                      tc::sdesc_sw128(kb + (kk >> 2) * Lay::kSlab + (kk & 3) * 32, 16, 1024), idS, kk > 0);
+        tc::commit(bar_s + (j & 1));
+        tc::commit(bar_empty + st);
+        return true;
+      };
+      auto issue_pv = [&](int j, bool first, int un) -> bool {
+        const int i = 2 * j + 1, st = i % nst;
+        if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
+        // P lands after the softmax warps have zeroed a last tile's V tail
+        if (!mbar_wait_bounded(bar_p + (j & 1), (j >> 1) & 1)) return false;
+        if (first && un > 0 && !mbar_wait_bounded(bar_o, (un - 1) & 1)) return false;
+        tc::fence_after();
+        const uint32_t vb = ring_a + st * Lay::kTile;
+#pragma unroll
+        for (int kk = 0; kk < kSpKeys / 16; ++kk)
+          tc::mma_f16_ts(tmem + 128, tmem + (j & 1) * 64 + kk * 8,
+                         tc::sdesc_sw128(vb + kk * 16 * 128, Lay::kSlab, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
+        tc::commit(bar_pv + (j & 1));
+        tc::commit(bar_empty + st);
+        return true;
+      };
+      bool ok = w.next();
+      int t = w.t0, j = 0, un = 0;
+      ok = ok && issue_s(0, true, 0);
+      while (ok) {
+        const bool last = t + 1 == w.t1;
+        if (!last) ok = issue_s(j + 1, false, un);
+        ok = ok && issue_pv(j, t == w.t0, un);
+        ++j;
+        ++t;
+        if (last) {
+          if (!w.next()) break;
+          t = w.t0;
+          ++un;
+          ok = ok && issue_s(j, true, un);
+        }
+      }
+    }
+  } else {
+    // ---- softmax: thread r owns query row r
+    const int r = tid;
+    const uint32_t tS = tmem + (static_cast<uint32_t>(warp * 32) << 16), tO = tS + 128;
+    const float c2 = p.scale_log2;
+    const uint64_t c2x2 = tc::f2(c2, c2);
+    constexpr float kSlack = 8.f, kLow = 8.f;  // as the prefill: P stays <= 2^8, and not all tiny
+    bool ok = true;
+    // A unit's Q into shared memory in the MMA's swizzled layout, 16-byte
+    // chunks copied asynchronously, all of a thread's in flight at once
+    auto load_q = [&]() {
+      constexpr int kCh = D / 8;
+      const uint32_t dst = smem_u32(sm);
+      const int sq0 = w.b0, h0 = w.kvh * p.group;
+      for (int i = tid; i < w.rows * kCh; i += kSpSoftWarps * 32) {
+        const int row = i / kCh, ch = i % kCh, sq = row / p.group;
+        cp_async16(dst + (ch >> 3) * Lay::kQSlab + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                   static_cast<const T*>(p.q) +
+                       (static_cast<int64_t>(sq0 + sq) * p.num_heads + h0 + row - sq * p.group) * D + ch * 8,
+                   true);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();  // read by the tensor cores
+      mbar_arrive(bar_q);
+    };
+    bool more = w.next();
+    if (more) load_q();
+    int j = 0;
+    while (more) {
+      const bool mine = warp * 32 < w.rows, valid = r < w.rows;
+      float m_ref = 0.f, l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++j) {
+        const int buf = (j & 1) * 64;
+        // after a timeout (recorded) the remaining waits are skipped
+        if (ok && !mbar_wait_bounded(bar_s + (j & 1), (j >> 1) & 1)) ok = false;
+        tc::fence_after();
+        const int keys = min(kSpKeys, w.keys - t * kSpKeys);
+        if (mine) {
+          uint32_t x[64];
+          uint64_t ls[2];
+          float me;
+          bool rescale = false;
+          float alpha = 1.f;
+          // one pass: e = S c2 - m_ref (no key: -inf), P = exp2(e) rounded
+          // to T, its sum, the row's max of e; repeated against a new
+          // reference only where that max calls for one
+#pragma unroll 1
+          for (int attempt = 0; attempt < 2; ++attempt) {
+            const uint64_t negm = tc::f2(-m_ref, -m_ref);
+            ls[0] = ls[1] = tc::f2(0.f, 0.f);
+            tc::ld_32x32b_x32(tS + buf, x);
+            tc::ld_32x32b_x32(tS + buf + 32, x + 32);
+            tc::wait_ld();
+            float ma = -INFINITY, mb = -INFINITY;
+            if (keys < kSpKeys) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float2 ev = tc::f2_split(
+                    tc::ffma2(tc::f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2x2, negm));
+                ev.x = 2 * i < keys ? ev.x : -INFINITY;
+                ev.y = 2 * i + 1 < keys ? ev.y : -INFINITY;
+                softmax_pair<T>(ev, i, ma, mb, ls, x);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                softmax_pair<T>(tc::f2_split(tc::ffma2(tc::f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                                       c2x2, negm)),
+                                i, ma, mb, ls, x);
+            }
+            me = fmaxf(ma, mb);
+            if (attempt == 1) break;
+            const bool need = valid && (me > kSlack || (l == 0.f && me != -INFINITY && me < -kLow));
+            rescale = __any_sync(0xffffffffu, need);
+            if (!rescale) break;
+            const float m_new = need ? m_ref + me : m_ref;
+            alpha = fast_exp2(m_ref - m_new);
+            l *= alpha;
+            m_ref = m_new;
+          }
+          tc::st_32x32b_x32(tS + buf, x);
+          const float2 a = tc::f2_split(ls[0]), b2 = tc::f2_split(ls[1]);
+          l += (a.x + a.y) + (b2.x + b2.y);
+          if (rescale && t > w.t0) {
+            // O holds the unit's tiles up to the last one: its P V is done
+            if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
+            tc::fence_after();
+            const uint64_t a2 = tc::f2(alpha, alpha);
+#pragma unroll
+            for (int oc = 0; oc < D; oc += 32) {
+              uint32_t v[32];
+              tc::ld_32x32b_x32(tO + oc, v);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 y = tc::f2_split(tc::fmul2(tc::f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), a2));
+                v[k] = __float_as_uint(y.x);
+                v[k + 1] = __float_as_uint(y.y);
+              }
+              tc::st_32x32b_x32(tO + oc, v);
+            }
+          }
+          tc::wait_st();
+        }
+        if (keys < kSpKeys) {
+          // V rows past the last key (blocks not loaded) are zeroed: their P
+          // is 0, and 0 times what lies there must be 0
+          const int i = 2 * j + 1, st = i % nst;
+          if (ok && !mbar_wait_bounded(bar_full + st, (i / nst) & 1)) ok = false;
+          uint8_t* vt = ring + st * Lay::kTile;
+#pragma unroll 1
+          for (int k = keys * 8 * kSlabs + tid; k < kSpKeys * 8 * kSlabs; k += kSpSoftWarps * 32) {
+            const int row = k / (8 * kSlabs), rest = k % (8 * kSlabs);
+            *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + row * 128 + (rest & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc::fence_before();
+        mbar_arrive(bar_p + (j & 1));
+      }
+      // all scores of the unit are read: the next unit's Q goes down while
+      // the last P V runs
+      const bool whole = w.t0 == 0 && w.t1 == w.T, begins = w.t0 == 0;
+      const int b0 = w.b0, kvh = w.kvh;
+      const int64_t end = w.at + kSpPrefixCost + w.T - 1;
+      more = w.next();
+      if (more) load_q();
+      if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
+      tc::fence_after();
+      if (mine) {
+        const int sq = r / p.group, b = b0 + sq, g = r - sq * p.group;
+        const int64_t orow = static_cast<int64_t>(b) * p.num_heads + kvh * p.group + g;
+        const int64_t crow = (static_cast<int64_t>(share) * 2 + (begins ? 1 : 0)) * kSpRows + r;
+        float* po = whole ? p.unit_o + orow * D : p.pre_o + crow * D;
+#pragma unroll 1
+        for (int oc = 0; oc < D; oc += 32) {
+          uint32_t v[32];
+          tc::ld_32x32b_x32(tO + oc, v);
+          tc::wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) st_global_32b(po + oc + k, v + k);
+          }
+        }
+        if (valid) {
+          *reinterpret_cast<float2*>(whole ? p.unit_ml + orow * 2 : p.pre_ml + crow * 2) = make_float2(m_ref, l);
+          // the unit's first CTA says where its pieces lie, once per sequence
+          if (g == 0 && begins)
+            p.pre_span[static_cast<int64_t>(b) * p.num_kv_heads + kvh] =
+                make_int4(share, whole ? share : sp_share_of(end, W, P), r, 0);
+        }
+      }
+      tc::fence_before();
+      mbar_arrive(bar_o);
+    }
+  }
+}
+
+// Registers: two CTAs of six warps, at most 168 a thread (as the prefill).
+// NG: n8 blocks of a rest unit's query rows.
+template <typename T, int D, int NG>
+__global__ void __launch_bounds__(kSpThreads, 2)
+    shared_prefix_kernel(const SpParams p, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmRK,
+                         const __grid_constant__ CUtensorMap tmRV) {
+  using Lay = SpLayout<D>;
+  extern __shared__ uint8_t sp_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sp_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Lay::kQ + p.stages * Lay::kTile);
+  uint64_t* rest_full = bars + 2 * kSpMaxStages + 8;  // [warp][rest stage] tile landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest_full + kSpSoftWarps * kSpMaxRest);
+  const int B = p.num_seqs, NGR = p.num_groups;
   SpLine ln;
-  ln.cum = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bar_full) + Lay::kBars);
-  ln.start = ln.cum + E + 1;
-  ln.prefix = ln.start + NG + 1;
-  ln.first = ln.prefix + NG;
+  ln.pre = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + Lay::kBars);
+  ln.rest = ln.pre + NGR + 1;
+  ln.start = ln.rest + B + 1;
+  ln.prefix = ln.start + NGR + 1;
+  ln.first = ln.prefix + NGR;
   ln.len = ln.first + B;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bs = p.block_size;
 
-  if (tid == 0) {
-    for (int s = 0; s < nst; ++s) {
-      mbar_init(bar_full + s, 1);
-      mbar_init(bar_empty + s, 1);
-    }
-    mbar_init(bar_q, kSpSoftWarps * 32);
-    mbar_init(bar_o, kSpSoftWarps * 32);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_s + i, 1);
-      mbar_init(bar_p + i, kSpSoftWarps * 32);
-      mbar_init(bar_pv + i, 1);
-    }
-    fence_mbar_init();
-  }
-  if (warp == kSpTmaWarp && lane == 0) {
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-  }
-  if (warp == kSpMmaWarp) tc::alloc(tmem_slot, kSpCols);
-
-  // ---- the line: lengths, groups, costs, their prefix sums (all global
+  // ---- the lines: lengths, groups, costs, their prefix sums (all global
   // loads before the first barrier)
   int bad = 0;
-  for (int g = tid; NG > 0 && g <= NG; g += kSpThreads) {
-    const int s = __ldg(p.group_start + g), nx = g < NG ? __ldg(p.group_start + g + 1) : B;
-    if (g < NG) ln.prefix[g] = __ldg(p.prefix_lens + g);
+#pragma unroll 4
+  for (int b = tid; b < B; b += kSpThreads) ln.len[b] = __ldg(p.seq_lens + b);
+  for (int g = tid; NGR > 0 && g <= NGR; g += kSpThreads) {
+    const int s = __ldg(p.group_start + g), nx = g < NGR ? __ldg(p.group_start + g + 1) : B;
+    if (g < NGR) ln.prefix[g] = __ldg(p.prefix_lens + g);
     ln.start[g] = s;
-    if (s < 0 || s > nx || nx > B || (g == 0 && s != 0) || (g == NG && s != B)) bad = 1;
+    if (s < 0 || s > nx || nx > B || (g == 0 && s != 0) || (g == NGR && s != B)) bad = 1;
   }
-  for (int b = tid; b < B; b += kSpThreads) ln.len[b] = sp_len(p, b);
+  if (tid == 0) {
+    uint64_t* bar = bars;
+    for (int s = 0; s < kSpMaxStages; ++s) {
+      mbar_init(bar + s, 1);
+      mbar_init(bar + kSpMaxStages + s, 1);
+    }
+    bar += 2 * kSpMaxStages;
+    mbar_init(bar, kSpSoftWarps * 32);      // Q
+    mbar_init(bar + 1, kSpSoftWarps * 32);  // O
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + 2 + i, 1);                  // S
+      mbar_init(bar + 4 + i, kSpSoftWarps * 32);  // P
+      mbar_init(bar + 6 + i, 1);                  // P V
+    }
+    for (int s = 0; s < kSpSoftWarps * kSpMaxRest; ++s) mbar_init(rest_full + s, 1);
+    fence_mbar_init();
+  }
+  if (warp == kSpTmaWarp && lane < 4)
+    prefetch_tensormap(lane == 0 ? &tmK : lane == 1 ? &tmV : lane == 2 ? &tmRK : &tmRV);
+  if (warp == kSpMmaWarp) tc::alloc(tmem_slot, kSpCols);
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) record_error(KV_ERR_DEVICE_BOUNDS);  // no group: every sequence reads its whole table
-  for (int g = tid; g < NG; g += kSpThreads) {
+  const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+  auto length = [&](int b) -> int {  // checked
+    const int L = ln.len[b];
+    return L < 0 ? 0 : L > cap ? static_cast<int>(cap) : L;
+  };
+  for (int g = tid; g < NGR; g += kSpThreads) {
     int P = 0, cost = 0;
     if (!bad) {
       const int n = ln.start[g + 1] - ln.start[g];
       if (ln.prefix[g] < 0) record_error(KV_ERR_DEVICE_BOUNDS);
       if (n > 1) {  // a group of one shares with nobody
-        P = max(0, min(ln.prefix[g], ln.len[ln.start[g]])) / bs * bs;
-        if (P > 0)
-          cost = (n + p.tile_seqs - 1) / p.tile_seqs * ((P + kSpKeys - 1) / kSpKeys + kSpUnitCost);
+        P = max(0, min(ln.prefix[g], length(ln.start[g]))) / bs * bs;
+        if (P > 0) cost = (n + p.tile_seqs - 1) / p.tile_seqs * ((P + kSpKeys - 1) / kSpKeys + kSpPrefixCost);
       }
     }
     ln.prefix[g] = P;
-    ln.cum[g + 1] = cost;
+    ln.pre[g + 1] = cost;
   }
   __syncthreads();
   for (int b = tid; b < B; b += kSpThreads) {
     int first = 0;
-    const int L = ln.len[b];
-    if (!bad && NG > 0) {
-      int lo = 0, hi = NG - 1;  // the last group that begins at or before b
+    const int L = length(b);
+    if (L != ln.len[b]) {
+      record_error(KV_ERR_DEVICE_BOUNDS);
+      ln.len[b] = L;
+    }
+    if (!bad && NGR > 0) {
+      int lo = 0, hi = NGR - 1;  // the last group that begins at or before b
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (ln.start[mid] <= b) lo = mid; else hi = mid - 1;
@@ -313,370 +788,71 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       if (L >= ln.prefix[lo]) first = ln.prefix[lo];
     }
     ln.first[b] = first;
-    ln.cum[NG + b + 1] = L > first ? (L - first + kSpKeys - 1) / kSpKeys + kSpUnitCost : 0;
+    ln.rest[b + 1] = L > first ? (L - first + kSpTok - 1) / kSpTok + kSpRestCost : 0;
     if (b % gridDim.x == blockIdx.x) p.seq[b] = make_int2(first, L);
   }
   __syncthreads();
   {
-    const int per = (E + kSpThreads - 1) / kSpThreads;
-    const int beg = min(E, tid * per), end = min(E, beg + per);
-    int local = 0;
-    for (int i = beg; i < end; ++i) local += ln.cum[i + 1];
-    int incl = local;
+    const int pg = (NGR + kSpThreads - 1) / kSpThreads, pb = (B + kSpThreads - 1) / kSpThreads;
+    const int g0 = min(NGR, tid * pg), g1 = min(NGR, g0 + pg), b0 = min(B, tid * pb), b1 = min(B, b0 + pb);
+    int lg = 0, lb = 0;
+    for (int i = g0; i < g1; ++i) lg += ln.pre[i + 1];
+    for (int i = b0; i < b1; ++i) lb += ln.rest[i + 1];
+    int ig = lg, ib = lb;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
+      const int yg = __shfl_up_sync(0xffffffffu, ig, off), yb = __shfl_up_sync(0xffffffffu, ib, off);
+      if (lane >= off) {
+        ig += yg;
+        ib += yb;
+      }
     }
-    __shared__ int warp_tot[kSpThreads / 32];
-    if (lane == 31) warp_tot[warp] = incl;
-    if (tid == 0) ln.cum[0] = 0;
+    __shared__ int2 warp_tot[kSpThreads / 32];
+    if (lane == 31) warp_tot[warp] = make_int2(ig, ib);
+    if (tid == 0) ln.pre[0] = ln.rest[0] = 0;
     __syncthreads();
-    int run = incl - local;
-    for (int w = 0; w < warp; ++w) run += warp_tot[w];
-    for (int i = beg; i < end; ++i) {
-      run += ln.cum[i + 1];
-      ln.cum[i + 1] = run;
+    ig -= lg;
+    ib -= lb;
+    for (int i = 0; i < warp; ++i) {
+      ig += warp_tot[i].x;
+      ib += warp_tot[i].y;
     }
+    for (int i = g0; i < g1; ++i) ln.pre[i + 1] = ig += ln.pre[i + 1];
+    for (int i = b0; i < b1; ++i) ln.rest[i + 1] = ib += ln.rest[i + 1];
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int64_t W = static_cast<int64_t>(p.num_kv_heads) * ln.cum[E];
-  const int P = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W)), pid = blockIdx.x;
-  const int64_t x0 = pid < P ? pid * W / P : 0, x1 = pid < P ? (pid + 1) * W / P : 0;
-
   // the merge kernel may be launched into what this one leaves free; it waits
   // for this grid's end itself
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (x0 < x1) {
-    SpWalk walk(p, ln, x0, x1);
-    SpUnit s;
-    if (warp == kSpTmaWarp) {
-      // ---- K and V tiles, one box of up to 64 rows per (block, 64-dim slab)
-      const int rpc = min(bs, kSpKeys);  // rows of a box
-      const int ci = lane / kSlabs, slab = lane % kSlabs;
-      // table entry of this lane's box of tile t and the box's offset in the
-      // block (-1: no box); the entry is looked at only when the box is copied
-      auto entry = [&](const SpUnit& un, int t, int& off) -> int {
-        const int tok = un.key0 + t * kSpKeys + ci * rpc;
-        off = -1;
-        if (ci * rpc >= kSpKeys || tok >= un.key1) return 0;
-        const int blk = tok / bs;
-        off = tok - blk * bs;
-        return __ldg(p.block_tables + static_cast<int64_t>(un.b0) * p.max_blocks_per_seq + blk);
-      };
-      // advances (unit, tile); false past the share's end
-      auto step = [&](SpUnit& un, int& t) -> bool {
-        if (++t < un.t1) return true;
-        if (!walk.next(un)) return false;
-        t = un.t0;
-        return true;
-      };
-      // the table entries of two tiles are in flight ahead of their copies
-      bool more = walk.next(s);
-      int t = s.t0, ok = 1, i = 0;
-      int off = -1, off1 = -1, off2 = -1;
-      int pb = more ? entry(s, t, off) : 0, kvh = s.kvh;
-      bool more1 = more && step(s, t);
-      int pb1 = more1 ? entry(s, t, off1) : 0, kvh1 = s.kvh;
-      while (more && ok) {
-        const bool more2 = more1 && step(s, t);
-        off2 = -1;
-        const int pb2 = more2 ? entry(s, t, off2) : 0, kvh2 = s.kvh;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, off >= 0));
-        if (off >= 0 && (pb < 0 || pb >= p.num_blocks)) {
-          record_error(KV_ERR_DEVICE_BOUNDS);
-          pb = 0;
-        }
-        const int row = pb * bs + off;
-        for (int v = 0; v < 2 && ok; ++v, ++i) {
-          const int st = i % nst;
-          if (lane == 0) {
-            if (i >= nst) ok = mbar_wait_bounded(bar_empty + st, (i / nst - 1) & 1);
-            if (ok) mbar_arrive_expect_tx(bar_full + st, static_cast<uint32_t>(boxes * rpc * 128));
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok && off >= 0)
-            tma_load_3d(ring + st * Lay::kTile + slab * Lay::kSlab + ci * rpc * 128, v ? &tmV : &tmK, bar_full + st,
-                        slab * 64, kvh, row);
-        }
-        pb = pb1, off = off1, kvh = kvh1, more = more1;
-        pb1 = pb2, off1 = off2, kvh1 = kvh2, more1 = more2;
-      }
-      // every stage's last MMAs have completed: no copy or commit in flight at exit
-      if (lane == 0 && ok)
-        for (int k = max(0, i - nst); k < i; ++k) mbar_wait_bounded(bar_empty + k % nst, (k / nst) & 1);
-    } else if (warp == kSpMmaWarp) {
-      if (lane == 0) {
-        // ---- MMA issue
-        constexpr uint32_t idS = tc::idesc_f16(kBf16, kSpRows, kSpKeys, false);
-        constexpr uint32_t idPV = tc::idesc_f16(kBf16, kSpRows, D, true);
-        const uint32_t aQ = smem_u32(sm), ring_a = smem_u32(ring);
-        // S of tile j (first: of unit number un) once its K, the unit's Q
-        // and its buffer (P V of tile j - 2 done) are ready
-        auto issue_s = [&](int j, bool first, int un) -> bool {
-          const int i = 2 * j, st = i % nst;
-          if (first && !mbar_wait_bounded(bar_q, un & 1)) return false;
-          if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
-          if (j >= 2 && !mbar_wait_bounded(bar_pv + (j & 1), ((j >> 1) - 1) & 1)) return false;
-          tc::fence_after();
-          const uint32_t kb = ring_a + st * Lay::kTile;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16(tmem + (j & 1) * 64,
-                        tc::sdesc_sw128(aQ + (kk >> 2) * Lay::kQSlab + (kk & 3) * 32, 16, 1024),
-                        tc::sdesc_sw128(kb + (kk >> 2) * Lay::kSlab + (kk & 3) * 32, 16, 1024), idS, kk > 0);
-          tc::commit(bar_s + (j & 1));
-          tc::commit(bar_empty + st);
-          return true;
-        };
-        auto issue_pv = [&](int j, bool first, int un) -> bool {
-          const int i = 2 * j + 1, st = i % nst;
-          if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
-          // P lands after the softmax warps have zeroed a last tile's V tail
-          if (!mbar_wait_bounded(bar_p + (j & 1), (j >> 1) & 1)) return false;
-          if (first && un > 0 && !mbar_wait_bounded(bar_o, (un - 1) & 1)) return false;
-          tc::fence_after();
-          const uint32_t vb = ring_a + st * Lay::kTile;
-#pragma unroll
-          for (int kk = 0; kk < kSpKeys / 16; ++kk)
-            tc::mma_f16_ts(tmem + 128, tmem + (j & 1) * 64 + kk * 8,
-                           tc::sdesc_sw128(vb + kk * 16 * 128, Lay::kSlab, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
-          tc::commit(bar_pv + (j & 1));
-          tc::commit(bar_empty + st);
-          return true;
-        };
-        bool more = walk.next(s);
-        int t = s.t0, j = 0, un = 0;
-        bool ok = more && issue_s(0, true, 0);
-        while (ok) {
-          const bool last = t + 1 == s.t1;
-          if (!last) ok = issue_s(j + 1, false, un);
-          ok = ok && issue_pv(j, t == s.t0, un);
-          ++j;
-          ++t;
-          if (last) {
-            if (!walk.next(s)) break;
-            t = s.t0;
-            ++un;
-            ok = ok && issue_s(j, true, un);
-          }
-        }
-      }
-    } else {
-      // ---- softmax: thread r owns query row r
-      const int r = tid;
-      const uint32_t tS = tmem + (static_cast<uint32_t>(warp * 32) << 16), tO = tS + 128;
-      const float c2 = p.scale_log2;
-      const uint64_t c2x2 = tc::f2(c2, c2);
-      constexpr float kSlack = 8.f, kLow = 8.f;  // as the prefill: P stays <= 2^8, and not all tiny
-      bool ok = true;
-      // A unit's Q goes to shared memory in the MMA's swizzled layout, 16-byte
-      // chunk i of the rows by thread i mod 128, loads in batches of kQBatch.
-      // The first batch (all of a rest unit's Q when G D <= 2048) is fetched
-      // while the unit before is still at work.
-      constexpr int kCh = D / 8, kQBatch = 2;
-      uint4 qv[kQBatch];
-      auto fetch_q = [&](const SpUnit& un, int i0) {
-#pragma unroll
-        for (int k = 0; k < kQBatch; ++k) {
-          const int i = i0 + k * kSpSoftWarps * 32;
-          if (i < un.rows * kCh) {
-            const int row = i / kCh, sq = row / p.group;
-            qv[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                         (static_cast<int64_t>(un.b0 + sq) * p.num_heads +
-                                                          un.kvh * p.group + row - sq * p.group) * D) +
-                          i % kCh);
-          }
-        }
-      };
-      auto store_q = [&](const SpUnit& un) {
-        for (int i0 = tid;; ) {
-#pragma unroll
-          for (int k = 0; k < kQBatch; ++k) {
-            const int i = i0 + k * kSpSoftWarps * 32;
-            if (i < un.rows * kCh) {
-              const int row = i / kCh, ch = i % kCh;
-              *reinterpret_cast<uint4*>(sm + (ch >> 3) * Lay::kQSlab + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
-                  qv[k];
-            }
-          }
-          i0 += kQBatch * kSpSoftWarps * 32;
-          if (i0 >= un.rows * kCh) break;
-          fetch_q(un, i0);
-        }
-        fence_proxy_async_smem();  // read by the tensor cores
-        mbar_arrive(bar_q);
-      };
-      bool more = walk.next(s);
-      if (more) {
-        fetch_q(s, tid);
-        store_q(s);
-      }
-      int j = 0;
-      while (more) {
-        const bool mine = warp * 32 < s.rows, valid = r < s.rows;
-        SpUnit nx;
-        bool nmore = false;
-        float m_ref = 0.f, l = 0.f;
-        for (int t = s.t0; t < s.t1; ++t, ++j) {
-          const int buf = (j & 1) * 64;
-          if (t + 1 == s.t1) {
-            nmore = walk.next(nx);
-            if (nmore) fetch_q(nx, tid);
-          }
-          // after a timeout (recorded) the remaining waits are skipped
-          if (ok && !mbar_wait_bounded(bar_s + (j & 1), (j >> 1) & 1)) ok = false;
-          tc::fence_after();
-          const int keys = min(kSpKeys, s.key1 - s.key0 - t * kSpKeys);
-          if (mine) {
-            uint32_t x[64];
-            uint64_t ls[2];
-            float me;
-            bool rescale = false;
-            float alpha = 1.f;
-            // one pass: e = S c2 - m_ref (no key: -inf), P = exp2(e) rounded
-            // to T, its sum, the row's max of e; repeated against a new
-            // reference only where that max calls for one
-#pragma unroll 1
-            for (int attempt = 0; attempt < 2; ++attempt) {
-              const uint64_t negm = tc::f2(-m_ref, -m_ref);
-              ls[0] = ls[1] = tc::f2(0.f, 0.f);
-              tc::ld_32x32b_x32(tS + buf, x);
-              tc::ld_32x32b_x32(tS + buf + 32, x + 32);
-              tc::wait_ld();
-              float ma = -INFINITY, mb = -INFINITY;
-              if (keys < kSpKeys) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  float2 ev = tc::f2_split(
-                      tc::ffma2(tc::f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2x2, negm));
-                  ev.x = 2 * i < keys ? ev.x : -INFINITY;
-                  ev.y = 2 * i + 1 < keys ? ev.y : -INFINITY;
-                  softmax_pair<T>(ev, i, ma, mb, ls, x);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  softmax_pair<T>(tc::f2_split(tc::ffma2(
-                                      tc::f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2x2, negm)),
-                                  i, ma, mb, ls, x);
-              }
-              me = fmaxf(ma, mb);
-              if (attempt == 1) break;
-              const bool need = valid && (me > kSlack || (l == 0.f && me != -INFINITY && me < -kLow));
-              rescale = __any_sync(0xffffffffu, need);
-              if (!rescale) break;
-              const float m_new = need ? m_ref + me : m_ref;
-              alpha = fast_exp2(m_ref - m_new);
-              l *= alpha;
-              m_ref = m_new;
-            }
-            tc::st_32x32b_x32(tS + buf, x);
-            const float2 a = tc::f2_split(ls[0]), b2 = tc::f2_split(ls[1]);
-            l += (a.x + a.y) + (b2.x + b2.y);
-            if (rescale && t > s.t0) {
-              // O holds the unit's tiles up to the last one: its P V is done
-              if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
-              tc::fence_after();
-              const uint64_t a2 = tc::f2(alpha, alpha);
-#pragma unroll
-              for (int oc = 0; oc < D; oc += 32) {
-                uint32_t w[32];
-                tc::ld_32x32b_x32(tO + oc, w);
-                tc::wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                  const float2 y =
-                      tc::f2_split(tc::fmul2(tc::f2(__uint_as_float(w[k]), __uint_as_float(w[k + 1])), a2));
-                  w[k] = __float_as_uint(y.x);
-                  w[k + 1] = __float_as_uint(y.y);
-                }
-                tc::st_32x32b_x32(tO + oc, w);
-              }
-            }
-            tc::wait_st();
-          }
-          if (keys < kSpKeys) {
-            // V rows past the last key (a block's tail, blocks not loaded) are
-            // zeroed: their P is 0, and 0 times what lies there must be 0
-            const int i = 2 * j + 1, st = i % nst;
-            if (ok && !mbar_wait_bounded(bar_full + st, (i / nst) & 1)) ok = false;
-            uint8_t* vt = ring + st * Lay::kTile;
-#pragma unroll 1
-            for (int k = keys * 8 * kSlabs + tid; k < kSpKeys * 8 * kSlabs; k += kSpSoftWarps * 32) {
-              const int row = k / (8 * kSlabs), rest = k % (8 * kSlabs);
-              *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + row * 128 + (rest & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-          tc::fence_before();
-          mbar_arrive(bar_p + (j & 1));
-        }
-        // all scores of the unit are read: the next unit's Q goes down while
-        // the last P V runs
-        const SpUnit d = s;
-        const float m_out = m_ref, l_out = l;
-        more = nmore;
-        if (more) {
-          s = nx;
-          store_q(s);
-        }
-        if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
-        tc::fence_after();
-        const bool whole = d.t0 == 0 && d.t1 == d.T;
-        const bool direct = whole && !d.prefix && d.key0 == 0;
-        if (mine) {
-          const int b = d.b0 + r / p.group, g = r % p.group, h = d.kvh * p.group + g;
-          const int64_t orow = static_cast<int64_t>(b) * p.num_heads + h;
-          const int64_t prow = (static_cast<int64_t>(pid) * 2 + (d.t0 == 0 ? 1 : 0)) * kSpRows + r;
-          const int64_t urow = orow + (d.prefix ? 0 : static_cast<int64_t>(p.num_seqs) * p.num_heads);
-          float* po = whole ? p.unit_o + urow * D : p.cut_o + prow * D;
-          float* pml = whole ? p.unit_ml + urow * 2 : p.cut_ml + prow * 2;
-          const float inv = l_out > 0.f ? __fdiv_rn(1.f, l_out) : 0.f;
-#pragma unroll 1
-          for (int oc = 0; oc < D; oc += 32) {
-            uint32_t w[32];
-            tc::ld_32x32b_x32(tO + oc, w);
-            tc::wait_ld();
-            if (valid && direct) {
-              uint4* o4 = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D + oc);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t y[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  y[c] = Mma<T>::pack(__uint_as_float(w[8 * k + 2 * c]) * inv,
-                                      __uint_as_float(w[8 * k + 2 * c + 1]) * inv);
-                o4[k] = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            } else if (valid) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) st_global_32b(po + oc + k, w + k);
-            }
-          }
-          if (valid && !direct) *reinterpret_cast<float2*>(pml) = make_float2(m_out, l_out);
-          // the unit's first CTA says where its pieces lie, once per sequence
-          if (valid && g == 0 && d.t0 == 0) {
-            const int a1 = whole ? pid : sp_cta_of(d.base + kSpUnitCost + d.T - 1, W, P);
-            (d.prefix ? p.pre_span : p.rest_span)[static_cast<int64_t>(b) * p.num_kv_heads + d.kvh] =
-                make_int4(pid, a1, r, 0);
-          }
-        }
-        tc::fence_before();
-        mbar_arrive(bar_o);
-      }
-    }
+
+  // ---- CTAs on each line, by weight
+  const int64_t Wp = static_cast<int64_t>(p.num_kv_heads) * ln.pre[NGR];
+  const int64_t Wr = static_cast<int64_t>(p.num_kv_heads) * ln.rest[B];
+  const int P = gridDim.x, pid = blockIdx.x;
+  int Pp = 0;
+  if (Wp > 0) {
+    const float tp = static_cast<float>(Wp) * kSpPrefixWeight, tr = static_cast<float>(Wr) * kSpRestWeight;
+    Pp = Wr == 0 ? P : max(1, min(P - 1, static_cast<int>(P * (tp / (tp + tr)) + 0.5f)));
+  }
+  if (pid < Pp) {
+    const int shares = static_cast<int>(min(static_cast<int64_t>(Pp), Wp));
+    if (pid < shares) prefix_cta<T, D>(p, ln, tmK, tmV, sm, bars, *tmem_slot, Wp, shares, pid);
+  } else if (warp < kSpSoftWarps && Wr > 0) {
+    // share s of the rest line goes to warp s / (P - Pp) of CTA Pp + s mod (P - Pp)
+    const int shares = static_cast<int>(min(static_cast<int64_t>(P - Pp) * kSpSoftWarps, Wr));
+    const int share = warp * (P - Pp) + pid - Pp;
+    if (share < shares)
+      rest_warp<T, D, NG>(p, ln, tmRK, tmRV, sm + warp * p.rest_stages * 2 * Lay::kRestTile,
+                          rest_full + warp * kSpMaxRest, Wr, shares, share, lane);
   }
   tc::fence_before();
   __syncthreads();
   if (warp == kSpMmaWarp) {
     __syncwarp();
     tc::fence_after();
-    tc::dealloc(tmem, kSpCols);
+    tc::dealloc(*tmem_slot, kSpCols);
   }
 }
 
@@ -703,14 +879,14 @@ __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const 
   const int64_t at = static_cast<int64_t>(b) * p.num_kv_heads + kvh;
   const int2 sq = p.seq[b];  // tokens from the prefix unit, length
   int4 ps = p.pre_span[at], rs = p.rest_span[at];
-  auto clamped = [&](int4 v) {  // CTAs in range whatever a call that timed out left there
-    v.x = max(0, min(v.x, p.num_ctas - 1));
-    v.y = max(v.x, min(v.y, p.num_ctas - 1));
+  auto clamped = [&](int4 v, int shares) {  // in range whatever a call that timed out left there
+    v.x = max(0, min(v.x, shares - 1));
+    v.y = max(v.x, min(v.y, shares - 1));
     v.z = max(0, min(v.z, kSpRows - p.group));
     return v;
   };
-  ps = sq.x > 0 ? clamped(ps) : make_int4(0, -1, 0, 0);
-  rs = sq.y > sq.x ? clamped(rs) : make_int4(0, -1, 0, 0);
+  ps = sq.x > 0 ? clamped(ps, p.num_ctas) : make_int4(0, -1, 0, 0);
+  rs = sq.y > sq.x ? clamped(rs, p.num_ctas * kSpSoftWarps) : make_int4(0, -1, 0, 0);
   const int np = ps.y - ps.x + 1, nr = rs.y - rs.x + 1;
   const bool skip = !real || (sq.x == 0 && nr == 1);  // written by the first kernel
   const int n = skip ? 0 : np + nr;
@@ -725,16 +901,18 @@ __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const 
       const int i = i0 + k * WPR;
       ml[k] = make_float2(-INFINITY, 0.f);
       if (i < n) {
-        // piece i: row of the whole units' array, or of a CTA's cut pieces
-        // (the first CTA's is its last piece, the others' their first)
+        // piece i: a row of the whole units' array, or of a share's cut pieces
+        // (the first share's is its last piece, the others' their first)
         const bool pre = i < np;
         const int4 s = pre ? ps : rs;
         const int c = pre ? i : i - np;
         const bool cut = s.x != s.y;
-        const int64_t pr = cut ? (static_cast<int64_t>(s.x + c) * 2 + (c == 0 ? 1 : 0)) * kSpRows + s.z + g
-                               : row + (pre ? 0 : static_cast<int64_t>(p.num_seqs) * p.num_heads);
-        ml[k] = *reinterpret_cast<const float2*>((cut ? p.cut_ml : p.unit_ml) + pr * 2);
-        const float* src = (cut ? p.cut_o : p.unit_o) + pr * D + lane * kV;
+        const int64_t slot = static_cast<int64_t>(s.x + c) * 2 + (c == 0 ? 1 : 0);
+        const int64_t pr = !cut  ? row + (pre ? 0 : static_cast<int64_t>(p.num_seqs) * p.num_heads)
+                           : pre ? slot * kSpRows + s.z + g
+                                 : slot * p.group + g;
+        ml[k] = *reinterpret_cast<const float2*>((!cut ? p.unit_ml : pre ? p.pre_ml : p.rest_ml) + pr * 2);
+        const float* src = (!cut ? p.unit_o : pre ? p.pre_o : p.rest_o) + pr * D + lane * kV;
         if constexpr (kV == 4) *reinterpret_cast<float4*>(y[k]) = *reinterpret_cast<const float4*>(src);
         else *reinterpret_cast<float2*>(y[k]) = *reinterpret_cast<const float2*>(src);
       }
@@ -799,10 +977,22 @@ PFN_cuTensorMapEncodeTiled_v12000 sp_encode_fn() {
 }
 
 // A layer's cache as a tensor {D, Hkv, slots}, boxes of 64 dims of one head
-// in `box_rows` consecutive slots, 128-byte swizzle.
-bool sp_map(const void* cache, int64_t slots, int hkv, int d, int box_rows, CUtensorMap* out) {
+// in `box_rows` consecutive slots; or (rest tiles) as {64, slots, D / 64, Hkv},
+// boxes of all D dims of one head in kSpTok slots, slab by slab.  128-byte
+// swizzle.
+bool sp_map(const void* cache, int64_t slots, int hkv, int d, int box_rows, bool rest, CUtensorMap* out) {
   auto fn = sp_encode_fn();
   if (!fn) return false;
+  if (rest) {
+    cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(slots), static_cast<cuuint64_t>(d / 64),
+                          static_cast<cuuint64_t>(hkv)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * d * 2, 128, static_cast<cuuint64_t>(d) * 2};
+    cuuint32_t box[4] = {64, kSpTok, static_cast<cuuint32_t>(d / 64), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hkv), static_cast<cuuint64_t>(slots)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(hkv) * d * 2};
   cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
@@ -823,18 +1013,18 @@ int sp_sm_count() {
 // paged_decode_attention.
 bool sp_shapes(int B, int G, int D, int bs, int dtype) {
   return dtype != KV_DTYPE_F32 && (D == 64 || D == 128) && (bs == 16 || bs == 32 || bs == 64 || bs == 128) &&
-         G <= kSpRows && B <= kSpMaxSeqs;
+         G <= kSpMaxGroup && B <= kSpMaxSeqs;
 }
-// The line's cost per kv head fits an int: at most 2 B units of the tiles of
-// a whole table row and the charge.
+// The lines' costs per kv head fit an int: at most B units of the tiles of a
+// whole table row and the charge.
 bool sp_line_fits(int B, int64_t row_tokens) {
-  return 2 * static_cast<int64_t>(B) * (row_tokens / kSpKeys + 1 + kSpUnitCost) < INT32_MAX;
+  return static_cast<int64_t>(B) * (row_tokens / kSpTok + 1 + std::max(kSpPrefixCost, kSpRestCost)) < INT32_MAX;
 }
 
 size_t sp_align(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct SpWorkspace {
-  size_t unit_o, unit_ml, cut_o, cut_ml, pre_span, rest_span, seq, bytes;
+  size_t unit_o, unit_ml, pre_o, pre_ml, rest_o, rest_ml, pre_span, rest_span, seq, bytes;
 };
 
 SpWorkspace sp_workspace(int B, int Hq, int Hkv, int D, int ctas) {
@@ -846,11 +1036,14 @@ SpWorkspace sp_workspace(int B, int Hq, int Hkv, int D, int ctas) {
     return here;
   };
   const size_t rows = static_cast<size_t>(B) * Hq, spans = static_cast<size_t>(B) * Hkv;
-  const size_t cuts = static_cast<size_t>(ctas) * 2 * kSpRows;
+  const size_t pre = static_cast<size_t>(ctas) * 2 * kSpRows;
+  const size_t rest = static_cast<size_t>(ctas) * kSpSoftWarps * 2 * (Hq / Hkv);
   w.unit_o = take(2 * rows * D * 4);
   w.unit_ml = take(2 * rows * 2 * 4);
-  w.cut_o = take(cuts * D * 4);
-  w.cut_ml = take(cuts * 2 * 4);
+  w.pre_o = take(pre * D * 4);
+  w.pre_ml = take(pre * 2 * 4);
+  w.rest_o = take(rest * D * 4);
+  w.rest_ml = take(rest * 2 * 4);
   w.pre_span = take(spans * sizeof(int4));
   w.rest_span = take(spans * sizeof(int4));
   w.seq = take(static_cast<size_t>(B) * sizeof(int2));
@@ -876,11 +1069,11 @@ cudaError_t launch_merge(const SpParams& p, int64_t rows, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, shared_merge_kernel<T, D, WPR>, p);
 }
 
-template <typename T, int D>
-cudaError_t launch_shared(SpParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t st) {
+template <typename T, int D, int NG>
+cudaError_t launch_shared(SpParams& p, const CUtensorMap (&maps)[4], int sms, cudaStream_t st) {
   using Lay = SpLayout<D>;
-  // as many stages as fit beside the batch's line (4 at head_dim 128, 8 at 64,
-  // for small batches); a batch whose line leaves no three gets an SM per CTA
+  // as many stages as fit beside the batch's lines (4 at head_dim 128, 8 at
+  // 64, for small batches); a batch whose lines leave no three gets an SM per CTA
   p.stages = D == 128 ? 4 : kSpMaxStages;
   while (p.stages > kSpMinStages && Lay::bytes(p.stages, p.num_seqs, p.num_groups) > kSpSmemTwo) --p.stages;
   int per_sm = 2;
@@ -889,14 +1082,15 @@ cudaError_t launch_shared(SpParams& p, const CUtensorMap& mk, const CUtensorMap&
     p.stages = D == 128 ? 4 : kSpMaxStages;
     while (p.stages > kSpMinStages && Lay::bytes(p.stages, p.num_seqs, p.num_groups) > kSpSmemOne) --p.stages;
   }
+  p.rest_stages = Lay::rest_stages(p.stages);
   const int smem = Lay::bytes(p.stages, p.num_seqs, p.num_groups);
   p.num_ctas = sms * per_sm;
-  auto kern = shared_prefix_kernel<T, D>;
+  auto kern = shared_prefix_kernel<T, D, NG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmemOne);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
-  kern<<<p.num_ctas, kSpThreads, smem, st>>>(p, mk, mv);
+  kern<<<p.num_ctas, kSpThreads, smem, st>>>(p, maps[0], maps[1], maps[2], maps[3]);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // few rows: up to eight warps join one
@@ -904,6 +1098,13 @@ cudaError_t launch_shared(SpParams& p, const CUtensorMap& mk, const CUtensorMap&
   if (rows * 8 <= static_cast<int64_t>(sms) * 64) return launch_merge<T, D, 8>(p, rows, st);
   if (rows * 2 <= static_cast<int64_t>(sms) * 64) return launch_merge<T, D, 2>(p, rows, st);
   return launch_merge<T, D, 1>(p, rows, st);
+}
+
+template <typename T>
+cudaError_t launch_shared_shape(SpParams& p, int head_dim, const CUtensorMap (&maps)[4], int sms, cudaStream_t st) {
+  if (head_dim == 64)
+    return p.group <= 8 ? launch_shared<T, 64, 1>(p, maps, sms, st) : launch_shared<T, 64, 2>(p, maps, sms, st);
+  return p.group <= 8 ? launch_shared<T, 128, 1>(p, maps, sms, st) : launch_shared<T, 128, 2>(p, maps, sms, st);
 }
 
 }  // namespace
@@ -975,25 +1176,22 @@ extern "C" int paged_decode_attention_shared_prefix(
   char* ws = static_cast<char*>(workspace);
   p.unit_o = reinterpret_cast<float*>(ws + w.unit_o);
   p.unit_ml = reinterpret_cast<float*>(ws + w.unit_ml);
-  p.cut_o = reinterpret_cast<float*>(ws + w.cut_o);
-  p.cut_ml = reinterpret_cast<float*>(ws + w.cut_ml);
+  p.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+  p.pre_ml = reinterpret_cast<float*>(ws + w.pre_ml);
+  p.rest_o = reinterpret_cast<float*>(ws + w.rest_o);
+  p.rest_ml = reinterpret_cast<float*>(ws + w.rest_ml);
   p.pre_span = reinterpret_cast<int4*>(ws + w.pre_span);
   p.rest_span = reinterpret_cast<int4*>(ws + w.rest_span);
   p.seq = reinterpret_cast<int2*>(ws + w.seq);
-  CUtensorMap mk, mv;
+  CUtensorMap maps[4];
   const int64_t slots = num_blocks * block_size;
   const int box = std::min(block_size, kSpKeys);
-  if (!sp_map(k_cache, slots, num_kv_heads, head_dim, box, &mk) ||
-      !sp_map(v_cache, slots, num_kv_heads, head_dim, box, &mv))
-    return cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled failed");
+  for (int i = 0; i < 4; ++i)
+    if (!sp_map(i & 1 ? v_cache : k_cache, slots, num_kv_heads, head_dim, box, i >= 2, &maps[i]))
+      return cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled failed");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == KV_DTYPE_F16)
-    e = head_dim == 64 ? launch_shared<__half, 64>(p, mk, mv, sms, st) : launch_shared<__half, 128>(p, mk, mv, sms, st);
-  else
-    e = head_dim == 64 ? launch_shared<__nv_bfloat16, 64>(p, mk, mv, sms, st)
-                       : launch_shared<__nv_bfloat16, 128>(p, mk, mv, sms, st);
-  return cuda_status(e);
+  return cuda_status(dtype == KV_DTYPE_F16 ? launch_shared_shape<__half>(p, head_dim, maps, sms, st)
+                                           : launch_shared_shape<__nv_bfloat16>(p, head_dim, maps, sms, st));
 }
 
 // Read (and optionally clear) this translation unit's device error word.
