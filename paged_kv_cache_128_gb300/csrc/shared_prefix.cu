@@ -43,7 +43,7 @@
 //     the last one's, and O += P V (N D) with P from tensor memory;
 //   warps 0-3: softmax, one query row per thread, as in the prefill: P, the
 //     sum and O are relative to a reference that moves only when a tile's
-//     maximum passes it by 2^8; warps without a row of the unit skip the
+//     maximum passes it by far; warps without a row of the unit skip the
 //     arithmetic.  They also lay a unit's Q into shared memory (any G: the
 //     rows are gathered) and write its results.
 // In a rest CTA each of warps 0-3 works by itself: its own ring of 16-token
@@ -540,7 +540,15 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
     const uint32_t tS = tmem + (static_cast<uint32_t>(warp * 32) << 16), tO = tS + 128;
     const float c2 = p.scale_log2;
     const uint64_t c2x2 = tc::f2(c2, c2);
-    constexpr float kSlack = 8.f, kLow = 8.f;  // as the prefill: P stays <= 2^8, and not all tiny
+    // A row's reference moves when a score passes it by more than kSlack (in
+    // powers of two), or when its first tile lies more than kLow below it.
+    // bf16 P has float32's exponents, so 2^30 costs no precision and the sums
+    // stay far from overflow (|V| < 2^90); fp16 P stays below 2^14 and its
+    // largest above 2^-8.  A move costs the warp a second pass and, past the
+    // unit's first tile, a wait for the last P V and a read and write of O
+    // (about 2 us): with 2^8 for both types, a warp of 32 rows of ordinary
+    // scores (standard deviation 1.5) moved in one tile of four.
+    constexpr float kSlack = kBf16 ? 30.f : 14.f, kLow = kBf16 ? 30.f : 8.f;
     bool ok = true;
     // A unit's Q into shared memory in the MMA's swizzled layout, 16-byte
     // chunks copied asynchronously, all of a thread's in flight at once
