@@ -142,35 +142,43 @@ struct SpLine {
 
 // The last entity of a line (cost prefix sums cum[0..n]) that begins at or
 // before place x < hkv cum[n]; it is not empty.
-__device__ __forceinline__ int sp_entity(const int* cum, int n, int hkv, int64_t x) {
+__device__ __forceinline__ int sp_entity(const int* cum, int n, int hkv, int x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(hkv) * cum[mid] <= x) lo = mid; else hi = mid - 1;
+    if (hkv * cum[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-// Of P shares [s W / P, (s + 1) W / P), the one that holds place t.
-__device__ __forceinline__ int sp_share_of(int64_t t, int64_t W, int P) {
-  return static_cast<int>(((t + 1) * P + W - 1) / W - 1);
-}
+// A line of length W cut into `shares` parts of W / shares places, the first
+// W mod shares of them one longer (the host has checked that places fit an
+// int).
+struct SpCut {
+  int shares, q, r;
+  __device__ __forceinline__ SpCut(int W, int most) : shares(min(W, most)), q(W / shares), r(W - q * shares) {}
+  __device__ __forceinline__ int begin(int s) const { return s * q + min(s, r); }
+  __device__ __forceinline__ int of(int place) const {  // the share that holds a place
+    const int longer = r * (q + 1);
+    return place < longer ? place / (q + 1) : r + (place - longer) / q;
+  }
+};
 
 // Prefix units of a share of the prefix line, in order.
 struct SpPrefixWalk {
   const SpParams& p;
   const SpLine& ln;
-  int64_t x, x1, base;  // place reached, the share's end, the unit's place
+  int x, x1, base;  // place reached, the share's end, the unit's place
   int e, u, cs, row_tiles, n;  // group, unit in it, a unit's cost, row tiles, sequences
   // the unit
   int b0, rows, kvh, keys, t0, t1, T;
-  int64_t at;
+  int at;
 
-  __device__ __forceinline__ SpPrefixWalk(const SpParams& p_, const SpLine& ln_, int64_t x0, int64_t x1_)
+  __device__ __forceinline__ SpPrefixWalk(const SpParams& p_, const SpLine& ln_, int x0, int x1_)
       : p(p_), ln(ln_), x(x0), x1(x1_) {
     enter(sp_entity(ln.pre, p.num_groups, p.num_kv_heads, x));
-    u = static_cast<int>((x - base) / cs);
-    base += static_cast<int64_t>(u) * cs;
+    u = (x - base) / cs;
+    base += u * cs;
   }
   __device__ __forceinline__ void enter(int g) {
     e = g;
@@ -178,14 +186,14 @@ struct SpPrefixWalk {
     n = ln.start[g + 1] - ln.start[g];
     row_tiles = (n + p.tile_seqs - 1) / p.tile_seqs;
     cs = (ln.pre[g + 1] - ln.pre[g]) / row_tiles;
-    base = static_cast<int64_t>(p.num_kv_heads) * ln.pre[g];
+    base = p.num_kv_heads * ln.pre[g];
   }
   // To the next unit with a tile in the share; false when there is none.
   __device__ __forceinline__ bool next() {
     while (x < x1) {
       T = cs - kSpPrefixCost;
-      t0 = static_cast<int>(max(static_cast<int64_t>(0), x - base - kSpPrefixCost));
-      t1 = static_cast<int>(min(static_cast<int64_t>(T), x1 - base - kSpPrefixCost));
+      t0 = max(0, x - base - kSpPrefixCost);
+      t1 = min(T, x1 - base - kSpPrefixCost);
       at = base;
       kvh = u / row_tiles;
       const int rt = u - kvh * row_tiles;
@@ -208,7 +216,7 @@ struct SpPrefixWalk {
 // Tiles of a share of the rest line, in order: tile t of unit (b, kvh).
 struct SpRestWalk {
   int b, kvh, t, t0, t1, T, first, len;
-  int64_t base, x1;
+  int base, x1;
 
   __device__ __forceinline__ void enter(const SpLine& ln, int b_) {
     b = b_;
@@ -216,19 +224,19 @@ struct SpRestWalk {
     first = ln.first[b];
     len = ln.len[b];
   }
-  __device__ __forceinline__ bool span(int64_t x) {  // tiles of the unit from place x on
-    t0 = static_cast<int>(max(static_cast<int64_t>(0), x - base - kSpRestCost));
-    t1 = static_cast<int>(min(static_cast<int64_t>(T), x1 - base - kSpRestCost));
+  __device__ __forceinline__ bool span(int x) {  // tiles of the unit from place x on
+    t0 = max(0, x - base - kSpRestCost);
+    t1 = min(T, x1 - base - kSpRestCost);
     t = t0;
     return t0 < t1;
   }
-  __device__ __forceinline__ bool begin(const SpParams& p, const SpLine& ln, int64_t x0, int64_t x1_) {
+  __device__ __forceinline__ bool begin(const SpParams& p, const SpLine& ln, int x0, int x1_) {
     x1 = x1_;
     if (x0 >= x1) return false;
     enter(ln, sp_entity(ln.rest, p.num_seqs, p.num_kv_heads, x0));
-    base = static_cast<int64_t>(p.num_kv_heads) * ln.rest[b];
-    kvh = static_cast<int>((x0 - base) / (T + kSpRestCost));
-    base += static_cast<int64_t>(kvh) * (T + kSpRestCost);
+    base = p.num_kv_heads * ln.rest[b];
+    kvh = (x0 - base) / (T + kSpRestCost);
+    base += kvh * (T + kSpRestCost);
     return span(x0) || next_unit(p, ln);
   }
   __device__ __forceinline__ bool next_unit(const SpParams& p, const SpLine& ln) {
@@ -247,22 +255,28 @@ struct SpRestWalk {
   }
 };
 
-// 32-byte store: a thread's piece of its row is a whole sector.
-__device__ __forceinline__ void st_global_32b(float* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+// Where 16-byte chunk c of row r of a prefix unit lies within the row in the
+// workspace: moved so that eight rows' chunks fall into different banks when
+// the rows are laid into shared memory for a bulk store.
+__device__ __forceinline__ int sp_chunk(int c, int r) { return c ^ (r & 7); }
+
+// Bulk store of contiguous shared memory, both ends 16-byte aligned.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
 
-// One warp's share [x0, x1) of the rest line; `share` is its index, P the
-// number of shares.
+// One warp's share of the rest line.
 template <typename T, int D, int NG>
 __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
-                                          const CUtensorMap& tmV, uint8_t* ring, uint64_t* full, int64_t W, int P,
+                                          const CUtensorMap& tmV, uint8_t* ring, uint64_t* full, const SpCut& cut,
                                           int share, int lane) {
   constexpr int kRestTile = SpLayout<D>::kRestTile;
   const int G = p.group, bs = p.block_size, nst = p.rest_stages;
-  const int64_t x0 = share * W / P, x1 = (share + 1) * W / P;
+  const int x0 = cut.begin(share), x1 = cut.begin(share + 1);
   SpRestWalk iw, cw;  // where the copies are, where the arithmetic is
   bool imore = iw.begin(p, ln, x0, x1);
   bool more = cw.begin(p, ln, x0, x1);
@@ -332,8 +346,8 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
     uint8_t* kt = ring + cst * 2 * kRestTile;
     consume_tile<T, D, kSpTok, NG>(st, kt, kt + kRestTile, cw.first + cw.t * kSpTok, cw.len, p.scale_log2, lane);
     __syncwarp();
-    ++done;
     if (imore) issue();  // into the stage just read
+    ++done;
     if (++cst == nst) {
       cst = 0;
       phase ^= 1;
@@ -380,7 +394,7 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
         }
       }
     if (cw.t0 == 0 && lane == 0) {  // the unit's first share says where its pieces lie
-      const int last = whole ? share : sp_share_of(cw.base + kSpRestCost + cw.T - 1, W, P);
+      const int last = whole ? share : cut.of(cw.base + kSpRestCost + cw.T - 1);
       p.rest_span[static_cast<int64_t>(cw.b) * p.num_kv_heads + cw.kvh] = make_int4(share, last, 0, 0);
     }
     more = cw.next_unit(p, ln);
@@ -408,7 +422,7 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
 template <typename T, int D>
 __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
                                            const CUtensorMap& tmV, uint8_t* sm, uint64_t* bars, uint32_t tmem,
-                                           int64_t W, int P, int share) {
+                                           const SpCut& cut, int share) {
   using Lay = SpLayout<D>;
   constexpr int kSlabs = Lay::kSlabs;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -422,7 +436,7 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
   uint64_t* bar_s = bar_o + 1;                    // [2] S written
   uint64_t* bar_p = bar_s + 2;                    // [2] P written (every softmax thread)
   uint64_t* bar_pv = bar_p + 2;                   // [2] P V done
-  SpPrefixWalk w(p, ln, share * W / P, (share + 1) * W / P);
+  SpPrefixWalk w(p, ln, cut.begin(share), cut.begin(share + 1));
   if (warp == kSpTmaWarp) {
     // ---- K and V tiles, one box of up to 64 rows per (block, 64-dim slab)
     const int rpc = min(bs, kSpKeys);  // rows of a box
@@ -668,16 +682,21 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
       // the last P V runs
       const bool whole = w.t0 == 0 && w.t1 == w.T, begins = w.t0 == 0;
       const int b0 = w.b0, kvh = w.kvh;
-      const int64_t end = w.at + kSpPrefixCost + w.T - 1;
+      const int end = w.at + kSpPrefixCost + w.T - 1, rows = w.rows;
       more = w.next();
       if (more) load_q();
       if (ok && !mbar_wait_bounded(bar_pv + ((j - 1) & 1), ((j - 1) >> 1) & 1)) ok = false;
       tc::fence_after();
+      // The results: after the CTA's last unit Q and the stages are free, and
+      // the rows go out through them in bulk stores (0.6 us for 128 rows of
+      // 128 floats; from the registers, 16 bytes of 32 rows at a time, 2.9 us);
+      // other units' rows are stored from the registers.
+      const int sq = r / p.group, b = b0 + sq, g = r - sq * p.group;
+      const int64_t orow = static_cast<int64_t>(b) * p.num_heads + kvh * p.group + g;
+      const int64_t crow = (static_cast<int64_t>(share) * 2 + (begins ? 1 : 0)) * kSpRows + r;
+      float* po = (whole ? p.unit_o + orow * D : p.pre_o + crow * D);
       if (mine) {
-        const int sq = r / p.group, b = b0 + sq, g = r - sq * p.group;
-        const int64_t orow = static_cast<int64_t>(b) * p.num_heads + kvh * p.group + g;
-        const int64_t crow = (static_cast<int64_t>(share) * 2 + (begins ? 1 : 0)) * kSpRows + r;
-        float* po = whole ? p.unit_o + orow * D : p.pre_o + crow * D;
+        uint4* dst = more ? reinterpret_cast<uint4*>(po) : reinterpret_cast<uint4*>(sm) + r * (D / 4);
 #pragma unroll 1
         for (int oc = 0; oc < D; oc += 32) {
           uint32_t v[32];
@@ -685,7 +704,8 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
           tc::wait_ld();
           if (valid) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) st_global_32b(po + oc + k, v + k);
+            for (int k = 0; k < 8; ++k)
+              dst[sp_chunk(oc / 4 + k, r)] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
         }
         if (valid) {
@@ -693,8 +713,16 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
           // the unit's first CTA says where its pieces lie, once per sequence
           if (g == 0 && begins)
             p.pre_span[static_cast<int64_t>(b) * p.num_kv_heads + kvh] =
-                make_int4(share, whole ? share : sp_share_of(end, W, P), r, 0);
+                make_int4(share, whole ? share : cut.of(end), r, 0);
         }
+      }
+      if (!more) {
+        fence_proxy_async_smem();
+        named_barrier_sync(1, kSpSoftWarps * 32);
+        // a cut unit's rows lie together; a whole one's sequence by sequence
+        if (!whole && r == 0) bulk_store(po, sm, static_cast<uint32_t>(rows * D * 4));
+        if (whole && valid && g == 0) bulk_store(po, sm + r * D * 4, static_cast<uint32_t>(p.group * D * 4));
+        bulk_store_wait();
       }
       tc::fence_before();
       mbar_arrive(bar_o);
@@ -797,9 +825,10 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     }
     ln.first[b] = first;
     ln.rest[b + 1] = L > first ? (L - first + kSpTok - 1) / kSpTok + kSpRestCost : 0;
-    if (b % gridDim.x == blockIdx.x) p.seq[b] = make_int2(first, L);
   }
   __syncthreads();
+  for (int b = blockIdx.x + tid * gridDim.x; b < B; b += kSpThreads * gridDim.x)
+    p.seq[b] = make_int2(ln.first[b], ln.len[b]);
   {
     const int pg = (NGR + kSpThreads - 1) / kSpThreads, pb = (B + kSpThreads - 1) / kSpThreads;
     const int g0 = min(NGR, tid * pg), g1 = min(NGR, g0 + pg), b0 = min(B, tid * pb), b1 = min(B, b0 + pb);
@@ -836,8 +865,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- CTAs on each line, by weight
-  const int64_t Wp = static_cast<int64_t>(p.num_kv_heads) * ln.pre[NGR];
-  const int64_t Wr = static_cast<int64_t>(p.num_kv_heads) * ln.rest[B];
+  const int Wp = p.num_kv_heads * ln.pre[NGR], Wr = p.num_kv_heads * ln.rest[B];
   const int P = gridDim.x, pid = blockIdx.x;
   int Pp = 0;
   if (Wp > 0) {
@@ -845,15 +873,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     Pp = Wr == 0 ? P : max(1, min(P - 1, static_cast<int>(P * (tp / (tp + tr)) + 0.5f)));
   }
   if (pid < Pp) {
-    const int shares = static_cast<int>(min(static_cast<int64_t>(Pp), Wp));
-    if (pid < shares) prefix_cta<T, D>(p, ln, tmK, tmV, sm, bars, *tmem_slot, Wp, shares, pid);
+    const SpCut cut(Wp, Pp);
+    if (pid < cut.shares) prefix_cta<T, D>(p, ln, tmK, tmV, sm, bars, *tmem_slot, cut, pid);
   } else if (warp < kSpSoftWarps && Wr > 0) {
     // share s of the rest line goes to warp s / (P - Pp) of CTA Pp + s mod (P - Pp)
-    const int shares = static_cast<int>(min(static_cast<int64_t>(P - Pp) * kSpSoftWarps, Wr));
+    const SpCut cut(Wr, (P - Pp) * kSpSoftWarps);
     const int share = warp * (P - Pp) + pid - Pp;
-    if (share < shares)
+    if (share < cut.shares)
       rest_warp<T, D, NG>(p, ln, tmRK, tmRV, sm + warp * p.rest_stages * 2 * Lay::kRestTile,
-                          rest_full + warp * kSpMaxRest, Wr, shares, share, lane);
+                          rest_full + warp * kSpMaxRest, cut, share, lane);
   }
   tc::fence_before();
   __syncthreads();
@@ -920,7 +948,9 @@ __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const 
                            : pre ? slot * kSpRows + s.z + g
                                  : slot * p.group + g;
         ml[k] = *reinterpret_cast<const float2*>((!cut ? p.unit_ml : pre ? p.pre_ml : p.rest_ml) + pr * 2);
-        const float* src = (!cut ? p.unit_o : pre ? p.pre_o : p.rest_o) + pr * D + lane * kV;
+        // a prefix row's 16-byte chunks are moved (sp_chunk)
+        const int at = pre ? sp_chunk(lane * kV / 4, s.z + g) * 4 + lane * kV % 4 : lane * kV;
+        const float* src = (!cut ? p.unit_o : pre ? p.pre_o : p.rest_o) + pr * D + at;
         if constexpr (kV == 4) *reinterpret_cast<float4*>(y[k]) = *reinterpret_cast<const float4*>(src);
         else *reinterpret_cast<float2*>(y[k]) = *reinterpret_cast<const float2*>(src);
       }
@@ -1023,10 +1053,12 @@ bool sp_shapes(int B, int G, int D, int bs, int dtype) {
   return dtype != KV_DTYPE_F32 && (D == 64 || D == 128) && (bs == 16 || bs == 32 || bs == 64 || bs == 128) &&
          G <= kSpMaxGroup && B <= kSpMaxSeqs;
 }
-// The lines' costs per kv head fit an int: at most B units of the tiles of a
-// whole table row and the charge.
-bool sp_line_fits(int B, int64_t row_tokens) {
-  return static_cast<int64_t>(B) * (row_tokens / kSpTok + 1 + std::max(kSpPrefixCost, kSpRestCost)) < INT32_MAX;
+// Places on the lines fit an int (with room for the units' places to be
+// stepped past the end): at most B units per kv head of the tiles of a whole
+// table row and the charge.
+bool sp_line_fits(int B, int Hkv, int64_t row_tokens) {
+  const int64_t unit = row_tokens / kSpTok + 1 + std::max(kSpPrefixCost, kSpRestCost);
+  return unit < (1 << 24) && unit * B < INT32_MAX / 2 / Hkv;
 }
 
 size_t sp_align(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1158,7 +1190,7 @@ extern "C" int paged_decode_attention_shared_prefix(
   }
   const int G = num_heads / num_kv_heads;
   if (!sp_shapes(num_seqs, G, head_dim, block_size, dtype) ||
-      !sp_line_fits(num_seqs, static_cast<int64_t>(max_blocks_per_seq) * block_size))
+      !sp_line_fits(num_seqs, num_kv_heads, static_cast<int64_t>(max_blocks_per_seq) * block_size))
     return paged_decode_attention(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads,
                                   head_dim, block_size, num_blocks, max_blocks_per_seq, max_seq_len, scale, 0, dtype,
                                   workspace, workspace_bytes, stream);
