@@ -27,5 +27,6 @@ def __getattr__(name):
                 "rope_and_cache", "rope_and_cache_fp8", "paged_decode_attention_shared_prefix",
                 "shared_prefix_workspace"):
         from . import kernels
-        return getattr(kernels, name)
+        value = globals()[name] = getattr(kernels, name)  # found directly from now on
+        return value
     raise AttributeError(name)

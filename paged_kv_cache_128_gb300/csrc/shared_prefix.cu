@@ -56,6 +56,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -1126,10 +1127,17 @@ cudaError_t launch_shared(SpParams& p, const CUtensorMap (&maps)[4], int sms, cu
   const int smem = Lay::bytes(p.stages, p.num_seqs, p.num_groups);
   p.num_ctas = sms * per_sm;
   auto kern = shared_prefix_kernel<T, D, NG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmemOne);
+  static std::atomic<uint64_t> configured{0};  // devices (of the first 64) whose limits are set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(configured.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmemOne);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured.fetch_or(uint64_t{1} << dev);
+  }
   kern<<<p.num_ctas, kSpThreads, smem, st>>>(p, maps[0], maps[1], maps[2], maps[3]);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -25,8 +25,10 @@ def dtype_code(dtype: torch.dtype) -> int:
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: building a Stream object costs 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -114,44 +116,53 @@ def reshape_and_cache_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tenso
                                             _stream_ptr(stream)), "paged_reshape_and_cache_fp8")
 
 
-def _same_device(named) -> int:
-    """Index of the one CUDA device that every (tensor, name) is on."""
-    dev = named[0][0].get_device()
-    for t, n in named:
-        d = t.get_device()
-        if d < 0:
-            raise KVError(1, f"{n} must be a CUDA tensor")
-        if d != dev:
-            raise KVError(1, f"{n} is on cuda:{d}, {named[0][1]} on cuda:{dev}")
-    return dev
+def _check_device(dev: int, tensors, names: str) -> None:
+    """Every tensor on CUDA device ``dev`` (``names``: their names, for the
+    refusal)."""
+    for i, t in enumerate(tensors):
+        if t.get_device() != dev or dev < 0:
+            n = names.split()[i]
+            raise KVError(1, f"{n} must be a CUDA tensor" if t.get_device() < 0 else
+                          f"{n} is on cuda:{t.get_device()}, another tensor on cuda:{dev}")
 
 
 def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping):
-    """Checks shared by the two rotating cache writes; (N, Hq, Hkv, D, bs,
-    NB, q strides)."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() \
-            or not v_cache.is_contiguous():
+    """Checks shared by the two rotating cache writes; the sizes of the call:
+    (N, Hq, Hkv, D, rot_dim, max_positions, bs, NB, token strides of q_out, q,
+    k and v)."""
+    _check_device(k_cache.get_device(), (k, v, positions, cos_sin, k_cache, v_cache, slot_mapping),
+                  "k v positions cos_sin k_cache v_cache slot_mapping")
+    shape, dt = k.shape, k.dtype
+    cache = k_cache.shape
+    if len(cache) != 4 or v_cache.shape != cache or not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise KVError(1, "caches must be contiguous [NB, BS, Hkv, D] of one shape")
-    nb, bs, hkv, d = k_cache.shape
+    nb, bs, hkv, d = cache
     n = slot_mapping.numel()
     if slot_mapping.dtype != torch.int32 or positions.dtype != torch.int32 or positions.numel() != n \
             or not slot_mapping.is_contiguous() or not positions.is_contiguous():
         raise KVError(1, "slot_mapping and positions must be contiguous int32 of one length")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise KVError(1, "cos_sin must be contiguous float32 [max_positions, rot_dim]")
-    for t in (k, v):
-        if t.dtype != k.dtype or t.shape != (n, hkv, d) or t.stride(2) != 1 or t.stride(1) != d:
-            raise KVError(1, "k and v must be [N, Hkv, D] of one dtype with dense heads")
+    if shape != (n, hkv, d) or v.shape != shape or v.dtype != dt:
+        raise KVError(1, "k and v must be [N, Hkv, D] of one dtype")
+    sk, sv = k.stride(), v.stride()
+    if sk[2] != 1 or sv[2] != 1 or sk[1] != d or sv[1] != d:
+        raise KVError(1, "k and v must have dense heads")
+    rows, rot = cos_sin.shape
     if q is None:
         if q_out is not None:
             raise KVError(1, "q_out without q")
-        return n, 0, hkv, d, bs, nb, 0, 0
-    hq = q.shape[1] if q.dim() == 3 else 0
-    for t in (q, q_out):
-        if t is None or t.dtype != k.dtype or t.shape != (n, hq, d) or t.stride(2) != 1 \
-                or (t.stride(1) != d and hq > 1):
-            raise KVError(1, "q and q_out must be [N, Hq, D] of k's dtype with dense heads")
-    return n, hq, hkv, d, bs, nb, q_out.stride(0), q.stride(0)
+        return n, 0, hkv, d, rot, rows, bs, nb, 0, 0, sk[0], sv[0]
+    if q_out is None:
+        raise KVError(1, "q without q_out")
+    _check_device(k_cache.get_device(), (q, q_out), "q q_out")
+    qs = q.shape
+    if len(qs) != 3 or q_out.shape != qs or qs[0] != n or qs[2] != d or q.dtype != dt or q_out.dtype != dt:
+        raise KVError(1, "q and q_out must be [N, Hq, D] of k's dtype")
+    sq, so = q.stride(), q_out.stride()
+    if sq[2] != 1 or so[2] != 1 or (qs[1] > 1 and (sq[1] != d or so[1] != d)):
+        raise KVError(1, "q and q_out must have dense heads")
+    return n, qs[1], hkv, d, rot, rows, bs, nb, so[0], sq[0], sk[0], sv[0]
 
 
 def rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -166,24 +177,20 @@ def rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: 
     position's angles; value pairs ``(i, i + rot_dim / 2)``, or ``(2i, 2i+1)``
     if ``interleaved``.  Token strides are free, ``q_out`` may be ``q``; q and
     q_out ``None``: only k and v."""
-    named = [(k, "k"), (v, "v"), (positions, "positions"), (cos_sin, "cos_sin"), (k_cache, "k_cache"),
-             (v_cache, "v_cache"), (slot_mapping, "slot_mapping")]
-    if q is not None:
-        named += [(q, "q")] + ([(q_out, "q_out")] if q_out is not None else [])
-    dev = _same_device(named)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    n, hq, hkv, d, rot, rows, bs, nb, so, sq, sk, sv = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache,
+                                                                  v_cache, slot_mapping)
+    dt = k.dtype
+    if k_cache.dtype != dt or v_cache.dtype != dt:
+        raise KVError(1, "k, v and the caches must share one dtype")
+    if k_cache.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(k_cache.device):
             return rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved,
                                   stream)
-    n, hq, hkv, d, bs, nb, so, sq = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping)
-    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
-        raise KVError(1, "k, v and the caches must share one dtype")
-    rows, rot = cos_sin.shape
     check(lib().paged_rope_and_cache(q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(),
                                      v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), k_cache.data_ptr(),
                                      v_cache.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, rot, rows,
-                                     1 if interleaved else 0, bs, nb, so, sq, k.stride(0), v.stride(0),
-                                     dtype_code(k.dtype), _stream_ptr(stream)), "paged_rope_and_cache")
+                                     1 if interleaved else 0, bs, nb, so, sq, sk, sv, dtype_code(dt),
+                                     _stream_ptr(stream)), "paged_rope_and_cache")
     return q_out
 
 
@@ -195,29 +202,25 @@ def rope_and_cache_fp8(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
     """``rope_and_cache`` into fp8 caches: E4M3 codes ``[NB, BS, Hkv, D]``
     (uint8) and float32 scales ``[NB, Hkv, BS]``, the rotated key quantised
     from float32; q, k, v fp16 or bf16."""
-    named = [(k, "k"), (v, "v"), (positions, "positions"), (cos_sin, "cos_sin"), (k_cache, "k_cache"),
-             (v_cache, "v_cache"), (k_scales, "k_scales"), (v_scales, "v_scales"), (slot_mapping, "slot_mapping")]
-    if q is not None:
-        named += [(q, "q")] + ([(q_out, "q_out")] if q_out is not None else [])
-    dev = _same_device(named)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return rope_and_cache_fp8(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, k_scales, v_scales,
-                                      slot_mapping, interleaved, stream)
-    n, hq, hkv, d, bs, nb, so, sq = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping)
+    n, hq, hkv, d, rot, rows, bs, nb, so, sq, sk, sv = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache,
+                                                                  v_cache, slot_mapping)
+    _check_device(k_cache.get_device(), (k_scales, v_scales), "k_scales v_scales")
     if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_scales.dtype != torch.float32 \
             or v_scales.dtype != torch.float32:
         raise KVError(1, "fp8 caches are uint8 codes with float32 scales")
     if k_scales.shape != (nb, hkv, bs) or v_scales.shape != (nb, hkv, bs) or not k_scales.is_contiguous() \
             or not v_scales.is_contiguous():
         raise KVError(1, "scales must be contiguous [NB, Hkv, BS]")
-    rows, rot = cos_sin.shape
+    if k_cache.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(k_cache.device):
+            return rope_and_cache_fp8(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, k_scales, v_scales,
+                                      slot_mapping, interleaved, stream)
     check(lib().paged_rope_and_cache_fp8(q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(),
                                          v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), k_cache.data_ptr(),
                                          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                          slot_mapping.data_ptr(), n, hq, hkv, d, rot, rows, 1 if interleaved else 0,
-                                         bs, nb, so, sq, k.stride(0), v.stride(0), dtype_code(k.dtype),
-                                         _stream_ptr(stream)), "paged_rope_and_cache_fp8")
+                                         bs, nb, so, sq, sk, sv, dtype_code(k.dtype), _stream_ptr(stream)),
+          "paged_rope_and_cache_fp8")
     return q_out
 
 
@@ -461,27 +464,26 @@ def paged_decode_attention_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_c
     ``KVBlockManager.prefix_groups``), which are read once for the group.
     ``workspace``: ``shared_prefix_workspace(...)`` (allocated here if
     omitted)."""
-    dev = _same_device(((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                        (block_tables, "block_tables"), (seq_lens, "seq_lens"), (group_start, "group_start"),
-                        (prefix_lens, "prefix_lens")))
-    if dev != torch.cuda.current_device():
+    dev = q.get_device()
+    _check_device(dev, (q, out, k_cache, v_cache, block_tables, seq_lens, group_start, prefix_lens),
+                  "q out k_cache v_cache block_tables seq_lens group_start prefix_lens")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise KVError(1, "q, out and caches must be contiguous")
+    for t in (block_tables, seq_lens, group_start, prefix_lens):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise KVError(1, "block_tables, seq_lens, group_start and prefix_lens must be contiguous int32")
+    shape, cache, dt = q.shape, k_cache.shape, q.dtype
+    if len(shape) != 3 or len(cache) != 4:
+        raise KVError(1, "q [B, Hq, D], caches [NB, BS, Hkv, D]")
+    B, hq, d = shape
+    nb, bs, hkv, d2 = cache
+    if d2 != d or out.shape != shape or v_cache.shape != cache or out.dtype != dt or k_cache.dtype != dt \
+            or v_cache.dtype != dt:
+        raise KVError(1, "shape or dtype mismatch")
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return paged_decode_attention_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, group_start,
                                                         prefix_lens, scale, max_seq_len, workspace, stream)
-    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise KVError(1, "q, out and caches must be contiguous")
-    for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (group_start, "group_start"),
-                 (prefix_lens, "prefix_lens")):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise KVError(1, f"{n} must be contiguous int32")
-    if q.dim() != 3 or k_cache.dim() != 4:
-        raise KVError(1, "q [B, Hq, D], caches [NB, BS, Hkv, D]")
-    B, hq, d = q.shape
-    nb, bs, hkv, d2 = k_cache.shape
-    dt = q.dtype
-    if d2 != d or out.shape != q.shape or v_cache.shape != k_cache.shape or out.dtype != dt or k_cache.dtype != dt \
-            or v_cache.dtype != dt:
-        raise KVError(1, "shape or dtype mismatch")
     groups = prefix_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B \
             or group_start.numel() != groups + 1:
