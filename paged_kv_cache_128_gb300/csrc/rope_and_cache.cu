@@ -12,7 +12,7 @@
 // the bit; it is rounded once more to the output type, or, for an fp8 cache,
 // quantised from float32 with no 16-bit rounding between ("paged-attention-
 // impl-detail", 实践建议 4: the row steps of the fp8 cache write).
-// A slot of -1 marks a padded token: nothing is read into or written for it
+// A slot of -1 marks a padded token: nothing is written for it
 // ("MiniPaged-Qwen" §11-§12, the cache write's rules).
 //
 // What bounds it: memory.  A token's q, k and v are read once, its q and its
@@ -24,11 +24,11 @@
 // c + R/2, or 16 consecutive values when interleaved).  D / 16 lanes make a
 // head and a CTA's thread count is a multiple of D / 16, so a thread keeps
 // one column, and one set of 8 cosines and sines in registers, over all the
-// heads it walks.  Heads come in rounds of kUnits whose loads all go out,
-// with the table row's, before any is used.  Few tokens: one CTA per token
-// and round of heads, so that a decode step's latency is one chain of loads
-// (position and slot, then rows and table, then the stores); many tokens: one
-// CTA per token walks all its heads.
+// heads it walks.  Heads come in rounds of kUnits whose loads all go out
+// before any is used, the first round's beside the position and the slot.
+// Few tokens: one CTA per token and round of heads, so that a decode step's
+// latency is one chain of loads (position, table row, then the stores); many
+// tokens: one CTA per token walks all its heads.
 
 #include <type_traits>
 
@@ -38,7 +38,15 @@ namespace pagedkv {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kUnits = 4;  // heads a thread has in flight
+// Heads a thread has in flight, and CTAs that must fit an SM (a bound on the
+// registers): warps in flight pay more than loads per thread.  32768 tokens of
+// 28 + 2 x 4 heads of 128, bf16: 122.7 us with four heads and no bound, 96.6
+// with one and twelve CTAs; 4581 tokens of 32 + 2 x 8 into fp8: 31.0 us, and
+// 23.2 with two and eight (whose rows need more registers).
+template <typename T, bool F8> struct RopeShape {
+  static constexpr int kUnits = F8 ? 2 : 1;
+  static constexpr int kCtas = F8 || sizeof(T) == 4 ? 8 : 12;
+};
 
 struct RopeParams {
   void* q_out;
@@ -118,7 +126,9 @@ __device__ __forceinline__ void rotate16(float (&x0)[8], float (&x1)[8], const f
 // quantised, a head's D / 16 lanes (4, 8 or 16, so within one warp) taking
 // the row's largest magnitude by shuffles.
 template <typename T, bool INTER, bool F8>
-__global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopeParams p, int threads) {
+__global__ void __launch_bounds__(kRopeThreads, (RopeShape<T, F8>::kCtas))
+rope_cache_kernel(const RopeParams p, int threads) {
+  constexpr int kUnits = RopeShape<T, F8>::kUnits;
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
   const int lph = p.head_dim >> 4;                     // lanes per head
@@ -148,8 +158,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopePara
       r[u][1].load(src + e1);
     }
   };
-  if (!rope_token(p, pos, slot, tid == 0 && blockIdx.y == 0)) return;
+  // the first heads' rows depend on neither position nor slot: their loads go
+  // out beside those (a padded token's rows are read and dropped)
   load(first);
+  if (!rope_token(p, pos, slot, tid == 0 && blockIdx.y == 0)) return;
   float c[8], s[8];
   if (turn) {
     const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.rot_dim + col * 8;
@@ -193,10 +205,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopePara
           r[u][0].get(x0);
           r[u][1].get(x1);
           if (turn && !is_v) rotate16<INTER>(x0, x1, c, s);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
         }
-        for (int o = lph >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (__any_sync(0xffffffffu, in && h >= p.num_heads)) {  // the warp holds K or V heads
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
+          }
+          for (int o = lph >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        }
         if (!in) continue;
         if (h < p.num_heads) {
           T* dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + h * p.head_dim;
@@ -297,6 +313,7 @@ cudaError_t launch_rope(const RopeParams& p, int64_t n, bool vec, cudaStream_t s
   }
   const int lph = p.head_dim / 16;
   const int threads = kRopeThreads / lph * lph;  // <= kRopeThreads: head_dim is at most 16 kRopeThreads
+  constexpr int kUnits = RopeShape<T, F8>::kUnits;
   const int rounds = (heads + threads / lph * kUnits - 1) / (threads / lph * kUnits);
   // all rounds side by side while the tokens alone leave SMs short of CTAs
   const int parts = n < sms * 8 ? (rounds < 65535 ? rounds : 65535) : 1;
