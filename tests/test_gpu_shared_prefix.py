@@ -133,6 +133,10 @@ CASES = [  # dtype, Hq, Hkv, D, bs, groups
     ("f16", 6, 2, 128, 32, [(6000, [1500, 3, 40])]),            # units cut many times over
     ("bf16", 32, 8, 128, 16, [(256, [1 + i % 7 for i in range(150)])]),  # many units of a tile each
     ("f16", 8, 8, 128, 16, [(48, [2, 1])] * 30),
+    ("bf16", 16, 2, 128, 32, [(1000, [20] * 33), (64, [3, 1] * 9)]),  # a pair of row tiles and one more; split units
+    ("f16", 8, 1, 64, 16, [(77, [1] * 31), (500, [9] * 17), (33, [4, 4])]),
+    ("bf16", 32, 2, 128, 16, [(300, [40, 2, 9] * 9)]),          # G 16: two n8 blocks
+    ("bf16", 64, 16, 64, 64, [(64, [5] * 3)] * 20),             # many units of one tile, split
 ]
 
 
@@ -326,8 +330,8 @@ def test_two_calls_at_once_on_two_streams():
     assert pk.device_error() == 0
 
 
-def test_wide_batches_take_fewer_stages_or_an_sm_each():
-    for n, hkv, groups in ((1700, 1, 1), (4096, 1, 512), (4100, 1, 2)):
+def test_wide_batches():
+    for n, hkv, groups in ((1700, 1, 1), (2048, 1, 512), (2048, 2, 2), (4096, 1, 512), (4100, 1, 2)):
         t = Batch("bf16", 4 * hkv, hkv, 128, 16, [(64, [1 + i % 3 for i in range(n // groups)])] * groups, seed=23)
         # every sequence a row of its own: check a spread of them
         t.run()
