@@ -37,7 +37,7 @@
 // A prefix CTA is the tcgen05 pipeline of the chunked prefill, at 64 keys a
 // tile and with two score buffers:
 //   warp 5: TMA: K and V tiles through the block table into one ring of
-//     stages, K_0 V_0 K_1 V_1 ..., across unit boundaries;
+//     stages, K_0 K_1 V_0 K_2 V_1 ..., across unit boundaries;
 //   warp 4: one lane issues the MMAs, M 128: S = Q K^T (N 64) into one of two
 //     buffers, so that the next tile's scores are made while the softmax is at
 //     the last one's, and O += P V (N D) with P from tensor memory;
@@ -85,7 +85,7 @@ constexpr int kSpTok = 16;       // tokens per rest tile
 constexpr int kSpMaxRest = 6;    // stages of a warp's ring of rest tiles
 // Charges, in tiles of the unit's line, for what a unit costs beyond its
 // tiles, and the weight of a prefix tile against a rest tile.
-constexpr int kSpPrefixCost = 4, kSpRestCost = 2;
+constexpr int kSpPrefixCost = 3, kSpRestCost = 2;
 constexpr int kSpPrefixWeight = 4, kSpRestWeight = 1;
 
 struct SpParams {
@@ -118,8 +118,9 @@ struct SpLayout {
   static constexpr int kSlabs = D / 64;
   static constexpr int kQSlab = kSpRows * 128;  // 64 dims of the 128 rows
   static constexpr int kQ = kSlabs * kQSlab;
-  static constexpr int kSlab = kSpKeys * 128;   // 64 dims of a tile's 64 keys
-  static constexpr int kTile = kSlabs * kSlab;
+  static constexpr int kAtom = 8 * 128;           // 64 dims of 8 keys
+  static constexpr int kEight = kSlabs * kAtom;   // 8 keys of a K or V tile, slab by slab
+  static constexpr int kTile = kSpKeys / 8 * kEight;
   static constexpr int kRestTile = kSpTok * D * 2;  // K or V of a rest tile
   static constexpr int kBars = 8 * (2 * kSpMaxStages + 8 + kSpSoftWarps * kSpMaxRest) + 64;
   // a rest CTA uses the bytes of Q and the stages for its warps' rings
@@ -312,8 +313,9 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
       }
       uint8_t* dst = ring + ist * 2 * kRestTile;
       mbar_arrive_expect_tx(full + ist, 2 * kRestTile);
-      tma_load_4d(dst, &tmK, full + ist, 0, pb * bs + off, 0, iw.kvh);
-      tma_load_4d(dst + kRestTile, &tmV, full + ist, 0, pb * bs + off, 0, iw.kvh);
+      const int at = (pb * bs + off) / kSpTok;
+      tma_load_5d(dst, &tmK, full + ist, 0, 0, 0, at, iw.kvh);
+      tma_load_5d(dst + kRestTile, &tmV, full + ist, 0, 0, 0, at, iw.kvh);
     }
     ++issued;
     if (++ist == nst) ist = 0;
@@ -439,55 +441,72 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
   uint64_t* bar_pv = bar_p + 2;                   // [2] P V done
   SpPrefixWalk w(p, ln, cut.begin(share), cut.begin(share + 1));
   if (warp == kSpTmaWarp) {
-    // ---- K and V tiles, one box of up to 64 rows per (block, 64-dim slab)
-    const int rpc = min(bs, kSpKeys);  // rows of a box
-    const int ci = lane / kSlabs, slab = lane % kSlabs;
+    // ---- K and V tiles, one box per block (up to 64 of its tokens by all
+    // dims).  A copy costs the warp some 58 clocks to issue, one after another
+    // whichever lanes issue them; boxes of 64 dims took twice as many.
+    const int rows = min(bs, kSpKeys), at = lane * rows;
+    const uint32_t box_bytes = static_cast<uint32_t>(rows / 8 * Lay::kEight);
     // Table entries are fetched 32 at a time, one per lane, and the row's next
     // 32 along with them: a load per tile held the tile's copies up by its
     // latency.
     auto fetch = [&](int seq, int chunk) -> int {
       const int e = (chunk << 5) + lane;
-      return e < p.max_blocks_per_seq ? p.block_tables[static_cast<int64_t>(seq) * p.max_blocks_per_seq + e] : 0;
+      return e < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + e)
+                                      : 0;
     };
     int have_b = -1, have_c = -1, mine = 0, next_c = -1, nxt = 0;
     int ok = 1, st = 0, phase = 0;
     bool wrapped = false;
+    const int shift = __ffs(bs) - 1;  // (a power of two)
+    // Copies go out in the order in which the MMA lane takes the tiles: K of
+    // the next tile before V of this one.  (In the order K V K V a K copy
+    // waited, behind the V copy before it, for a P V that its own stage did
+    // not need.)
+    auto copy = [&](const CUtensorMap& map, bool box, int eight, uint32_t bytes) {
+      if (lane == 0) {
+        if (wrapped) ok = mbar_wait_bounded(bar_empty + st, phase ^ 1);
+        if (ok) mbar_arrive_expect_tx(bar_full + st, bytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) return;
+      if (box)
+        tma_load_5d(ring + st * Lay::kTile + (at >> 3) * Lay::kEight, &map, bar_full + st, 0, 0, 0, eight, w.kvh);
+      if (++st == nst) {
+        st = 0;
+        phase ^= 1;
+        wrapped = true;
+      }
+    };
     while (ok && w.next()) {
+      bool v_box = false;  // the V copy that is due
+      int v_eight = 0;
+      uint32_t v_bytes = 0;
       for (int t = w.t0; t < w.t1 && ok; ++t) {
-        const int tok = t * kSpKeys, c = tok / bs >> 5;  // a tile's blocks lie in one chunk
+        const int tok = t * kSpKeys, c = tok >> shift >> 5;  // a tile's blocks lie in one chunk
         if (w.b0 != have_b || c != have_c) {
           mine = w.b0 == have_b && c == next_c ? nxt : fetch(w.b0, c);
           have_b = w.b0;
           have_c = c;
-          next_c = (c + 1 << 5) * bs < w.keys ? c + 1 : 0;  // the row's next chunk; after its last, the next head's first
+          // the row's next chunk; after its last, the first again (the next head's)
+          next_c = (c + 1) * 32 < (w.keys + bs - 1) >> shift ? c + 1 : 0;
           if (next_c != have_c) nxt = fetch(have_b, next_c);
         }
-        const int here = tok + ci * rpc;
-        const bool box = ci * rpc < kSpKeys && here < w.keys;
-        const int blk = here / bs;
-        int pb = __shfl_sync(0xffffffffu, mine, blk & 31);
-        const int boxes = __popc(__ballot_sync(0xffffffffu, box));
+        const int here = tok + at;
+        const bool box = at < kSpKeys && here < w.keys;
+        int pb = __shfl_sync(0xffffffffu, mine, here >> shift & 31);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * box_bytes;
         if (box && (pb < 0 || pb >= p.num_blocks)) {
           record_error(KV_ERR_DEVICE_BOUNDS);
           pb = 0;
         }
-        const int row = pb * bs + here - blk * bs;
-        for (int v = 0; v < 2 && ok; ++v) {
-          if (lane == 0) {
-            if (wrapped) ok = mbar_wait_bounded(bar_empty + st, phase ^ 1);
-            if (ok) mbar_arrive_expect_tx(bar_full + st, static_cast<uint32_t>(boxes * rpc * 128));
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok && box)
-            tma_load_3d(ring + st * Lay::kTile + slab * Lay::kSlab + ci * rpc * 128, v ? &tmV : &tmK, bar_full + st,
-                        slab * 64, w.kvh, row);
-          if (ok && ++st == nst) {
-            st = 0;
-            phase ^= 1;
-            wrapped = true;
-          }
-        }
+        const int eight = ((pb << shift) + (here & (bs - 1))) >> 3;
+        copy(tmK, box, eight, bytes);
+        if (ok && t > w.t0) copy(tmV, v_box, v_eight, v_bytes);
+        v_box = box;
+        v_eight = eight;
+        v_bytes = bytes;
       }
+      if (ok) copy(tmV, v_box, v_eight, v_bytes);
     }
     // every stage's last MMAs have completed: no copy or commit in flight at exit
     if (lane == 0 && ok)
@@ -498,38 +517,47 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
       // ---- MMA issue
       constexpr uint32_t idS = tc::idesc_f16(kBf16, kSpRows, kSpKeys, false);
       constexpr uint32_t idPV = tc::idesc_f16(kBf16, kSpRows, D, true);
-      const uint32_t aQ = smem_u32(sm), ring_a = smem_u32(ring);
+      constexpr uint32_t kQHi = tc::sdesc_hi(1024), kKvHi = tc::sdesc_hi(Lay::kEight);
+      const uint32_t q_lo = tc::sdesc_lo(smem_u32(sm), 16), k_lo = tc::sdesc_lo(smem_u32(ring), 16);
+      const uint32_t v_lo = tc::sdesc_lo(smem_u32(ring), Lay::kAtom);
+      int st = 0, phase = 0;  // the ring's stage that is taken next
+      auto taken = [&]() {
+        tc::commit(bar_empty + st);
+        if (++st == nst) {
+          st = 0;
+          phase ^= 1;
+        }
+      };
       // S of tile j (first: of unit number un) once its K, the unit's Q
       // and its buffer (P V of tile j - 2 done) are ready
       auto issue_s = [&](int j, bool first, int un) -> bool {
-        const int i = 2 * j, st = i % nst;
         if (first && !mbar_wait_bounded(bar_q, un & 1)) return false;
-        if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
+        if (!mbar_wait_bounded(bar_full + st, phase)) return false;
         if (j >= 2 && !mbar_wait_bounded(bar_pv + (j & 1), ((j >> 1) - 1) & 1)) return false;
         tc::fence_after();
-        const uint32_t kb = ring_a + st * Lay::kTile;
+        const uint32_t d = tmem + (j & 1) * 64, kb = k_lo + st * (Lay::kTile / 16);
+        tc::mma_f16_words<false>(d, q_lo, kQHi, kb, kKvHi, idS);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_f16(tmem + (j & 1) * 64, tc::sdesc_sw128(aQ + (kk >> 2) * Lay::kQSlab + (kk & 3) * 32, 16, 1024),
-                      tc::sdesc_sw128(kb + (kk >> 2) * Lay::kSlab + (kk & 3) * 32, 16, 1024), idS, kk > 0);
+        for (int kk = 1; kk < D / 16; ++kk)
+          tc::mma_f16_words<true>(d, q_lo + ((kk >> 2) * Lay::kQSlab + (kk & 3) * 32) / 16, kQHi,
+                                  kb + ((kk >> 2) * Lay::kAtom + (kk & 3) * 32) / 16, kKvHi, idS);
         tc::commit(bar_s + (j & 1));
-        tc::commit(bar_empty + st);
+        taken();
         return true;
       };
       auto issue_pv = [&](int j, bool first, int un) -> bool {
-        const int i = 2 * j + 1, st = i % nst;
-        if (!mbar_wait_bounded(bar_full + st, (i / nst) & 1)) return false;
+        if (!mbar_wait_bounded(bar_full + st, phase)) return false;
         // P lands after the softmax warps have zeroed a last tile's V tail
         if (!mbar_wait_bounded(bar_p + (j & 1), (j >> 1) & 1)) return false;
         if (first && un > 0 && !mbar_wait_bounded(bar_o, (un - 1) & 1)) return false;
         tc::fence_after();
-        const uint32_t vb = ring_a + st * Lay::kTile;
+        const uint32_t a = tmem + (j & 1) * 64, vb = v_lo + st * (Lay::kTile / 16);
 #pragma unroll
         for (int kk = 0; kk < kSpKeys / 16; ++kk)
-          tc::mma_f16_ts(tmem + 128, tmem + (j & 1) * 64 + kk * 8,
-                         tc::sdesc_sw128(vb + kk * 16 * 128, Lay::kSlab, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
+          tc::mma_f16_ts_words(tmem + 128, a + kk * 8, vb + kk * (2 * Lay::kEight / 16), kKvHi, idPV,
+                               (!first || kk > 0) ? 1u : 0u);
         tc::commit(bar_pv + (j & 1));
-        tc::commit(bar_empty + st);
+        taken();
         return true;
       };
       bool ok = w.next();
@@ -665,14 +693,14 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
         if (keys < kSpKeys) {
           // V rows past the last key (blocks not loaded) are zeroed: their P
           // is 0, and 0 times what lies there must be 0
-          const int i = 2 * j + 1, st = i % nst;
+          const int i = 2 * j + 1, st = i % nst;  // (the unit's last tile: no K lies before its V)
           if (ok && !mbar_wait_bounded(bar_full + st, (i / nst) & 1)) ok = false;
           uint8_t* vt = ring + st * Lay::kTile;
 #pragma unroll 1
           for (int k = keys * 8 * kSlabs + tid; k < kSpKeys * 8 * kSlabs; k += kSpSoftWarps * 32) {
             const int row = k / (8 * kSlabs), rest = k % (8 * kSlabs);
-            *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + row * 128 + (rest & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(vt + (row >> 3) * Lay::kEight + (rest >> 3) * Lay::kAtom + (row & 7) * 128 +
+                                      (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -1003,28 +1031,21 @@ PFN_cuTensorMapEncodeTiled_v12000 sp_encode_fn() {
   return fn;
 }
 
-// A layer's cache as a tensor {D, Hkv, slots}, boxes of 64 dims of one head
-// in `box_rows` consecutive slots; or (rest tiles) as {64, slots, D / 64, Hkv},
-// boxes of all D dims of one head in kSpTok slots, slab by slab.  128-byte
-// swizzle.
-bool sp_map(const void* cache, int64_t slots, int hkv, int d, int box_rows, bool rest, CUtensorMap* out) {
+// A layer's cache as a tensor {64 dims, `rows` slots, D / 64 slabs, slots /
+// rows, Hkv}, boxes of all D dims of one head in `groups` times `rows`
+// consecutive slots (a block's slots are a multiple of `rows`): shared memory
+// holds `rows` slots slab by slab, then the next ones.  128-byte swizzle.
+bool sp_map(const void* cache, int64_t slots, int hkv, int d, int rows, int groups, CUtensorMap* out) {
   auto fn = sp_encode_fn();
   if (!fn) return false;
-  if (rest) {
-    cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(slots), static_cast<cuuint64_t>(d / 64),
-                          static_cast<cuuint64_t>(hkv)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * d * 2, 128, static_cast<cuuint64_t>(d) * 2};
-    cuuint32_t box[4] = {64, kSpTok, static_cast<cuuint32_t>(d / 64), 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  }
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hkv), static_cast<cuuint64_t>(slots)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(hkv) * d * 2};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(cache), dims, strides, box, estr,
+  const cuuint64_t slot = static_cast<cuuint64_t>(hkv) * d * 2;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(d / 64),
+                        static_cast<cuuint64_t>(slots / rows), static_cast<cuuint64_t>(hkv)};
+  cuuint64_t strides[4] = {slot, 128, slot * rows, static_cast<cuuint64_t>(d) * 2};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(d / 64),
+                       static_cast<cuuint32_t>(groups), 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void*>(cache), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1213,12 +1234,14 @@ extern "C" int paged_decode_attention_shared_prefix(
   p.pre_span = reinterpret_cast<int4*>(ws + w.pre_span);
   p.rest_span = reinterpret_cast<int4*>(ws + w.rest_span);
   p.seq = reinterpret_cast<int2*>(ws + w.seq);
-  CUtensorMap maps[4];
+  CUtensorMap maps[4];  // prefix K, V; rest K, V
   const int64_t slots = num_blocks * block_size;
-  const int box = std::min(block_size, kSpKeys);
-  for (int i = 0; i < 4; ++i)
-    if (!sp_map(i & 1 ? v_cache : k_cache, slots, num_kv_heads, head_dim, box, i >= 2, &maps[i]))
-      return cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled failed");
+  const int rows = std::min(block_size, kSpKeys);
+  if (!sp_map(k_cache, slots, num_kv_heads, head_dim, 8, rows / 8, &maps[0]) ||
+      !sp_map(v_cache, slots, num_kv_heads, head_dim, 8, rows / 8, &maps[1]) ||
+      !sp_map(k_cache, slots, num_kv_heads, head_dim, kSpTok, 1, &maps[2]) ||
+      !sp_map(v_cache, slots, num_kv_heads, head_dim, kSpTok, 1, &maps[3]))
+    return cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled failed");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status(dtype == KV_DTYPE_F16 ? launch_shared_shape<__half>(p, head_dim, maps, sms, st)
                                            : launch_shared_shape<__nv_bfloat16>(p, head_dim, maps, sms, st));
