@@ -146,13 +146,15 @@ def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mappin
     if shape != (n, hkv, d) or v.shape != shape or v.dtype != dt:
         raise KVError(1, "k and v must be [N, Hkv, D] of one dtype")
     sk, sv = k.stride(), v.stride()
-    if sk[2] != 1 or sv[2] != 1 or sk[1] != d or sv[1] != d:
+    if sk[2] != 1 or sv[2] != 1 or (hkv > 1 and (sk[1] != d or sv[1] != d)):
         raise KVError(1, "k and v must have dense heads")
+    # one token's or one head's stride is anything (a transposed view's, say)
+    sk, sv = (sk[0], sv[0]) if n > 1 else (hkv * d, hkv * d)
     rows, rot = cos_sin.shape
     if q is None:
         if q_out is not None:
             raise KVError(1, "q_out without q")
-        return n, 0, hkv, d, rot, rows, bs, nb, 0, 0, sk[0], sv[0]
+        return n, 0, hkv, d, rot, rows, bs, nb, 0, 0, sk, sv
     if q_out is None:
         raise KVError(1, "q without q_out")
     _check_device(k_cache.get_device(), (q, q_out), "q q_out")
@@ -162,7 +164,8 @@ def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mappin
     sq, so = q.stride(), q_out.stride()
     if sq[2] != 1 or so[2] != 1 or (qs[1] > 1 and (sq[1] != d or so[1] != d)):
         raise KVError(1, "q and q_out must have dense heads")
-    return n, qs[1], hkv, d, rot, rows, bs, nb, so[0], sq[0], sk[0], sv[0]
+    so, sq = (so[0], sq[0]) if n > 1 else (qs[1] * d, qs[1] * d)
+    return n, qs[1], hkv, d, rot, rows, bs, nb, so, sq, sk, sv
 
 
 def rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,

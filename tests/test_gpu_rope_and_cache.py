@@ -265,3 +265,27 @@ def test_rope_wrapper_refusals():
             with pytest.raises(pk.KVError) as e:
                 pk.rope_and_cache(**{**good, name: x})
             assert e.value.code == "INVALID_ARG", name
+
+
+@pytest.mark.parametrize("n,hq,hkv", [(1, 8, 2), (6, 1, 1), (1, 1, 1)])
+def test_rope_one_token_or_one_head_of_a_transposed_tensor(n, hq, hkv):
+    """[heads, tokens, D] transposed: dense rows whose other stride (of a
+    single token, of a single head) is not that of a dense [N, H, D]."""
+    c = _case("bf16", n, hq, hkv, 64, 64, 16, 0, seed=5)
+    dev = torch.device("cuda")
+
+    def turned(t):
+        t = t.transpose(0, 1).clone(memory_format=torch.contiguous_format)
+        if t.shape[0] == 1:  # a single head: one of a larger tensor, its own stride 2 N D
+            t = torch.cat([t, t], 1)[:, :n]
+        return t.transpose(0, 1)
+
+    rest = (_dev(c["pos"]), _dev(c["table"]))
+    caches = [torch.zeros(c["nb"], 16, hkv, 64, dtype=torch.bfloat16, device=dev) for _ in range(4)]
+    q, k, v = (turned(c[x]) for x in "qkv")
+    assert q.stride()[:2] != (hq * 64, 64) and k.stride()[:2] != (hkv * 64, 64)
+    a = pk.rope_and_cache(torch.zeros_like(c["q"].contiguous()), c["q"].contiguous(), c["k"].contiguous(),
+                          c["v"].contiguous(), *rest, caches[0], caches[1], _dev(c["slots"]))
+    b = pk.rope_and_cache(torch.zeros_like(q), q, k, v, *rest, caches[2], caches[3], _dev(c["slots"]))
+    assert torch.equal(a, b) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    assert pk.device_error() == 0
