@@ -29,6 +29,11 @@
 // Few tokens: one CTA per token and round of heads, so that a decode step's
 // latency is one chain of loads (position, table row, then the stores); many
 // tokens: one CTA per token walks all its heads.
+//
+// Measured on the device: 32768 tokens of 28 + 2 x 4 heads of 128, bf16: 96.7
+// us, 621 MB, 0.95 of the copy rate; 4581 of 32 + 2 x 8: 19.7 us (0.82), into
+// fp8 caches 23.1 us (0.64; 20.8 with a product in the place of the correctly
+// rounded divisions that the codes' definition asks for); 8 tokens: 2.0 us.
 
 #include <type_traits>
 
