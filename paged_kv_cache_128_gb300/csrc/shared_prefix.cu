@@ -188,8 +188,9 @@ struct SpPrefixWalk {
   const SpLine& ln;
   int x, x1, base;  // place reached, the share's end, the unit's place
   int e, u, cs, row_tiles, n;  // group, unit in it, a unit's cost, row tiles, sequences
-  // the unit
-  int b0, rows, kvh, keys, t0, t1, T;
+  // the unit; lead: the group's first sequence, whose table row holds the prefix (b0, the row tile's first, may
+  // be shorter than the prefix, or empty, and its row another)
+  int b0, lead, rows, kvh, keys, t0, t1, T;
   int at;
 
   __device__ __forceinline__ SpPrefixWalk(const SpParams& p_, const SpLine& ln_, int x0, int x1_)
@@ -215,7 +216,8 @@ struct SpPrefixWalk {
       at = base;
       kvh = u / row_tiles;
       const int rt = u - kvh * row_tiles;
-      b0 = ln.start[e] + rt * p.tile_seqs;
+      lead = ln.start[e];
+      b0 = lead + rt * p.tile_seqs;
       rows = min(p.tile_seqs, n - rt * p.tile_seqs) * p.group;
       keys = ln.prefix[e];
       base += cs;
@@ -464,7 +466,7 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
     const uint32_t box_bytes = static_cast<uint32_t>(rows / 8 * Lay::kEight);
     // Table entries are fetched 32 at a time, one per lane, and the row's next
     // 32 along with them: a load per tile held the tile's copies up by its
-    // latency.
+    // latency.  All of a group's units read its first sequence's row.
     auto fetch = [&](int seq, int chunk) -> int {
       const int e = (chunk << 5) + lane;
       return e < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + e)
@@ -499,11 +501,11 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
       uint32_t v_bytes = 0;
       for (int t = w.t0; t < w.t1 && ok; ++t) {
         const int tok = t * kSpKeys, c = tok >> shift >> 5;  // a tile's blocks lie in one chunk
-        if (w.b0 != have_b || c != have_c) {
-          mine = w.b0 == have_b && c == next_c ? nxt : fetch(w.b0, c);
-          have_b = w.b0;
+        if (w.lead != have_b || c != have_c) {
+          mine = w.lead == have_b && c == next_c ? nxt : fetch(w.lead, c);
+          have_b = w.lead;
           have_c = c;
-          // the row's next chunk; after its last, the first again (the next head's)
+          // the row's next chunk; after its last, the first again (the next unit's)
           next_c = (c + 1) * 32 < (w.keys + bs - 1) >> shift ? c + 1 : 0;
           if (next_c != have_c) nxt = fetch(have_b, next_c);
         }
