@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (!rescale) break;
         // a row that does not need it keeps its reference (alpha 1)
         const float m_new = need ? m_ref + me : m_ref;
-        alpha = fast_exp2(m_ref - m_new);
+        // before the row's first key of weight l and O are 0: nothing to
+        // rescale, and a move down by 2^128 or more would make it 0 inf
+        alpha = l == 0.f ? 1.f : fast_exp2(m_ref - m_new);
         l *= alpha;
         m_ref = m_new;
       }
