@@ -994,7 +994,9 @@ __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const 
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (!(ml[k].y > 0.f)) continue;  // no such piece, or one without weight
+      // no such piece, or one without weight; a piece whose sum is NaN (a score
+      // that is NaN or +inf) makes the row NaN
+      if (ml[k].y == 0.f) continue;
       const float mx = fmaxf(m, ml[k].x);
       const float old = fast_exp2(m - mx), wt = fast_exp2(ml[k].x - mx);
       m = mx;
@@ -1017,7 +1019,7 @@ __global__ void __launch_bounds__(kSpMergeWarps * 32) shared_merge_kernel(const 
 #pragma unroll
     for (int k = 1; k < WPR; ++k) {
       const float mk = part[rw][k][D], dk = part[rw][k][D + 1];
-      if (!(dk > 0.f)) continue;
+      if (dk == 0.f) continue;
       const float mx = fmaxf(m, mk), old = fast_exp2(m - mx), wt = fast_exp2(mk - mx);
       m = mx;
       den = den * old + wt * dk;
