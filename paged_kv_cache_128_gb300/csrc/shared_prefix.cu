@@ -604,12 +604,15 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
     // A row's reference moves when a score passes it by more than kSlack (in
     // powers of two), or when its first tile lies more than kLow below it.
     // bf16 P has float32's exponents, so 2^30 costs no precision and the sums
-    // stay far from overflow (|V| < 2^90); fp16 P stays below 2^14 and its
-    // largest above 2^-8.  A move costs the warp a second pass and, past the
-    // unit's first tile, a wait for the last P V and a read and write of O
-    // (about 2 us): with 2^8 for both types, a warp of 32 rows of ordinary
-    // scores (standard deviation 1.5) moved in one tile of four.
-    constexpr float kSlack = kBf16 ? 30.f : 14.f, kLow = kBf16 ? 30.f : 8.f;
+    // stay far from overflow (|V| < 2^90).  fp16 P stays below 2^14, and its
+    // largest is 1 or more, so that weights down to 2^-25 of the largest count
+    // (rounded to P's step of 2^-24), as in the decode kernels; with the
+    // largest at 2^-8 those below 2^-17 of it were lost.  A move costs the
+    // warp a second pass and, past the unit's first tile, a wait for the last
+    // P V and a read and write of O (about 2 us): with 2^8 for both types, a
+    // warp of 32 rows of ordinary scores (standard deviation 1.5) moved in one
+    // tile of four.
+    constexpr float kSlack = kBf16 ? 30.f : 14.f, kLow = kBf16 ? 30.f : 0.f;
     bool ok = true;
     // A unit's Q into shared memory in the MMA's swizzled layout, 16-byte
     // chunks copied asynchronously, all of a thread's in flight at once
