@@ -485,10 +485,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int lim_abs = min(ctx + tok0 + tok, nkeys - 1);  // last key the row sees
     const float c2 = p.scale_log2;
     const uint64_t c2x2 = tc::f2(c2, c2);
-    // a reference at most 2^8 below the row's max keeps P <= 256; before
-    // the row's first key it is also at most 2^8 above it, so the largest P
-    // keeps its precision in fp16 too
-    constexpr float kSlack = 8.f, kLow = 8.f;
+    // a reference at most 2^8 below the row's max keeps P <= 256; at the
+    // row's first key it is at most 2^8 above it in bf16, which has the
+    // exponents for it, and not above it in fp16, whose P then is 1 or more at
+    // its largest: weights down to 2^-25 of that count (with 2^8 there too,
+    // those below 2^-17 were lost)
+    constexpr float kSlack = 8.f, kLow = kBf16 ? 8.f : 0.f;
     // P, O and the sum are relative to m_ref, 0 until the row's scores
     // call for another
     float m_ref = 0.f, l = 0.f;
