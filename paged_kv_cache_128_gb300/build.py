@@ -17,7 +17,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libpagedkv.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 HEADERS = [os.path.join(ROOT, "include", "pagedkv.h"), os.path.join(CSRC, "common.cuh"),
-           os.path.join(CSRC, "tcgen05.cuh"), os.path.join(CSRC, "decode_tile.cuh")]
+           os.path.join(CSRC, "tcgen05.cuh"), os.path.join(CSRC, "decode_tile.cuh"),
+           os.path.join(CSRC, "stage_ring.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CUDA_SOURCES = ["reshape_and_cache.cu", "paged_decode.cu", "paged_prefill.cu", "step_runner.cu",

@@ -43,6 +43,9 @@ inline size_t dtype_bytes(int dtype) { return dtype == KV_DTYPE_F32 ? 4 : 2; }
 // Last CUDA error met by an entry point on this thread (see kv_last_cuda_error).
 const char*& last_cuda_error_text();
 
+// KV_DEBUG_SKIP_TILE as set by kv_debug_set (-1: off).
+int32_t debug_skip_tile();
+
 // Map a CUDA result to a status, remembering the error text on failure.
 inline int cuda_status(cudaError_t e, const char* what = nullptr) {
   if (e == cudaSuccess) return KV_OK;

@@ -1668,7 +1668,8 @@ uint64_t next_epoch() {
   return base + 2 * (counter.fetch_add(1) + 1);
 }
 
-// Stream-K test controls (kv_debug_set), read at each launch.
+// Stream-K test controls (kv_debug_set), read at each launch; the
+// shared-prefix kernel reads skip_tile too.
 struct SkControls {
   std::atomic<int64_t> wait_limit_ns{static_cast<int64_t>(kWaitLimitNs)};
   std::atomic<int64_t> skip_tile{-1};
@@ -1933,7 +1934,7 @@ cudaError_t launch_sk(DecodeParams& p, const CUtensorMap& mk, const CUtensorMap&
   p.epoch = next_epoch();
   p.seg_cost = seg_cost_tiles(C::TL::kStageBytes, F8);
   p.wait_limit_ns = static_cast<uint64_t>(sk_controls().wait_limit_ns.load());
-  p.test_skip_tile = static_cast<int32_t>(sk_controls().skip_tile.load());
+  p.test_skip_tile = debug_skip_tile();
   // Cooperative: the driver refuses the launch unless all CTAs can be
   // resident at once, which the owners' waits on later CTAs rely on.
   cudaLaunchConfig_t cfg{};
@@ -2472,6 +2473,8 @@ extern "C" int kv_debug_set(int key, int64_t value) {
 extern "C" const char* kv_version(void) { return "pagedkv-gb300 0.1 (sm_103a)"; }
 
 namespace pagedkv {
+int32_t debug_skip_tile() { return static_cast<int32_t>(sk_controls().skip_tile.load()); }
+
 const char*& last_cuda_error_text() {
   static thread_local const char* text = "no error";
   return text;

@@ -79,6 +79,7 @@
 
 #include "common.cuh"
 #include "decode_tile.cuh"
+#include "stage_ring.h"
 #include "tcgen05.cuh"
 
 namespace pagedkv {
@@ -117,6 +118,7 @@ struct SpParams {
   int32_t stages, rest_stages;
   float scale_log2;  // scale * log2(e)
   int32_t num_sms, num_ctas;
+  int32_t test_skip;  // test control (-1: off): the prefix line's first share never loads this copy
   // workspace
   float* unit_o;   // [2][B][Hq][D] whole units: prefix, rest
   float* unit_ml;  // [2][B][Hq][2] (reference, sum)
@@ -138,7 +140,7 @@ struct SpLayout {
   static constexpr int kEight = kSlabs * kAtom;   // 8 keys of a K or V tile, slab by slab
   static constexpr int kTile = kSpKeys / 8 * kEight;
   static constexpr int kRestTile = kSpTok * D * 2;  // K or V of a rest tile
-  static constexpr int kBars = 8 * (2 * kSpMaxStages + 8 + kSpSoftWarps * kSpMaxRest) + 64;
+  static constexpr int kBars = 8 * (2 * kSpMaxStages + 9 + kSpSoftWarps * kSpMaxRest) + 56;
   // a rest CTA uses the bytes of Q and the stages for its warps' rings
   static int rest_stages(int stages) {
     return std::min(kSpMaxRest, (kQ + stages * kTile) / (kSpSoftWarps * 2 * kRestTile));
@@ -289,6 +291,17 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// The phases of a ring's last fills, each waited for (bounded): up to the
+// first wait that runs out, or all of them.  Not inlined, for the registers
+// of the loops before it (inlined: 64 sequences on 4096 tokens 29.9 us, not 29.0).
+__device__ __noinline__ bool sp_drain(uint64_t* bars, int armed, int stages, bool all) {
+  bool ok = true;
+  fills_in_flight(armed, stages, [&](int s, int parity) {
+    if ((ok || all) && !mbar_wait_bounded(bars + s, parity)) ok = false;
+  });
+  return ok;
+}
+
 // One warp's share of the rest line.
 template <typename T, int D, int NG>
 __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
@@ -358,7 +371,7 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
     fetch_next_q();
   }
   reset_state(st);
-  int cst = 0, phase = 0, ok = 1, done = 0;
+  int cst = 0, phase = 0, ok = 1;
   while (more && ok) {
     if (lane == 0) ok = mbar_wait_bounded(full + cst, phase);
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -368,7 +381,6 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
     consume_tile<T, D, kSpTok, NG>(st, kt, kt + kRestTile, cw.first + cw.t * kSpTok, cw.len, p.scale_log2, lane);
     __syncwarp();
     if (imore) issue();  // into the stage just read
-    ++done;
     if (++cst == nst) {
       cst = 0;
       phase ^= 1;
@@ -435,8 +447,7 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
       reset_state(st);
     }
   }
-  if (!ok && lane == 0)  // a wait ran out: let the copies in flight land (bounded) before the CTA ends
-    for (int i = done + 1; i < issued; ++i) mbar_wait_bounded(full + i % nst, (i / nst) & 1);
+  if (!ok && lane == 0) sp_drain(full, issued, nst, true);  // a wait ran out: no copy in flight as the CTA ends
 }
 
 // A CTA's share [x0, x1) of the prefix line.
@@ -457,6 +468,7 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
   uint64_t* bar_s = bar_o + 1;                    // [2] S written
   uint64_t* bar_p = bar_s + 2;                    // [2] P written (every softmax thread)
   uint64_t* bar_pv = bar_p + 2;                   // [2] P V done
+  uint64_t* bar_end = bar_pv + 2;                 // after a wait ran out: all MMAs done
   SpPrefixWalk w(p, ln, cut.begin(share), cut.begin(share + 1));
   if (warp == kSpTmaWarp) {
     // ---- K and V tiles, one box per block (up to 64 of its tokens by all
@@ -473,8 +485,8 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
                                       : 0;
     };
     int have_b = -1, have_c = -1, mine = 0, next_c = -1, nxt = 0;
-    int ok = 1, st = 0, phase = 0;
-    bool wrapped = false;
+    const int skip = share == 0 ? p.test_skip : -1;
+    int ok = 1, st = 0, phase = 0, armed = 0;
     const int shift = __ffs(bs) - 1;  // (a power of two)
     // Copies go out in the order in which the MMA lane takes the tiles: K of
     // the next tile before V of this one.  (In the order K V K V a K copy
@@ -482,17 +494,17 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
     // not need.)
     auto copy = [&](const CUtensorMap& map, bool box, int eight, uint32_t bytes) {
       if (lane == 0) {
-        if (wrapped) ok = mbar_wait_bounded(bar_empty + st, phase ^ 1);
-        if (ok) mbar_arrive_expect_tx(bar_full + st, bytes);
+        if (armed >= nst) ok = mbar_wait_bounded(bar_empty + st, phase ^ 1);
+        if (ok && armed != skip) mbar_arrive_expect_tx(bar_full + st, bytes);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) return;
-      if (box)
+      if (box && armed != skip)
         tma_load_5d(ring + st * Lay::kTile + (at >> 3) * Lay::kEight, &map, bar_full + st, 0, 0, 0, eight, w.kvh);
+      ++armed;
       if (++st == nst) {
         st = 0;
         phase ^= 1;
-        wrapped = true;
       }
     };
     while (ok && w.next()) {
@@ -526,10 +538,12 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
       }
       if (ok) copy(tmV, v_box, v_eight, v_bytes);
     }
-    // every stage's last MMAs have completed: no copy or commit in flight at exit
-    if (lane == 0 && ok)
-      for (int k = 0; k < nst; ++k)
-        if (k < st || wrapped) mbar_wait_bounded(bar_empty + k, k < st ? phase : phase ^ 1);
+    // At exit no copy or commit is in flight: every stage's last MMAs have
+    // completed, or, where a wait ran out (the MMA lane may be gone), at least
+    // the copies have landed.
+    if (lane == 0) {
+      if (!ok || !sp_drain(bar_empty, armed, nst, false)) sp_drain(bar_full, armed, nst, true);
+    }
   } else if (warp == kSpMmaWarp) {
     if (lane == 0) {
       // ---- MMA issue
@@ -578,9 +592,9 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
         taken();
         return true;
       };
-      bool ok = w.next();
+      const bool any = w.next();
       int t = w.t0, j = 0, un = 0;
-      ok = ok && issue_s(0, true, 0);
+      bool ok = any && issue_s(0, true, 0);
       while (ok) {
         const bool last = t + 1 == w.t1;
         if (!last) ok = issue_s(j + 1, false, un);
@@ -593,6 +607,10 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
           ++un;
           ok = ok && issue_s(j, true, un);
         }
+      }
+      if (any && !ok) {  // a wait ran out: what was issued ends before the tensor memory goes
+        tc::commit(bar_end);
+        mbar_wait_bounded(bar_end, 0);
       }
     }
   } else {
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   extern __shared__ uint8_t sp_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sp_smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Lay::kQ + p.stages * Lay::kTile);
-  uint64_t* rest_full = bars + 2 * kSpMaxStages + 8;  // [warp][rest stage] tile landed
+  uint64_t* rest_full = bars + 2 * kSpMaxStages + 9;  // [warp][rest stage] tile landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest_full + kSpSoftWarps * kSpMaxRest);
   const int B = p.num_seqs, NGR = p.num_groups;
   SpLine ln;
@@ -811,8 +829,8 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   if (warp == kSpTmaWarp) {
     if (lane < 4) prefetch_tensormap(lane == 0 ? &tmK : lane == 1 ? &tmV : lane == 2 ? &tmRK : &tmRV);
     for (int s = lane; s < 2 * kSpMaxStages; s += 32) mbar_init(bars + s, 1);
-    // Q and O: every softmax thread; S, P (every softmax thread) and P V of two buffers
-    if (lane < 8) mbar_init(bars + 2 * kSpMaxStages + lane, lane < 2 || (lane >= 4 && lane < 6) ? kSpSoftWarps * 32 : 1);
+    // Q and O: every softmax thread; S, P (every softmax thread) and P V of two buffers; the end
+    if (lane < 9) mbar_init(bars + 2 * kSpMaxStages + lane, lane < 2 || (lane >= 4 && lane < 6) ? kSpSoftWarps * 32 : 1);
     for (int s = lane; s < kSpSoftWarps * kSpMaxRest; s += 32) mbar_init(rest_full + s, 1);
     fence_mbar_init();
   }
@@ -1247,6 +1265,7 @@ extern "C" int paged_decode_attention_shared_prefix(
   p.num_blocks = num_blocks;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.test_skip = debug_skip_tile();
   const int sms = sp_sm_count();
   const SpWorkspace w = sp_workspace(num_seqs, num_heads, num_kv_heads, head_dim, 2 * sms);
   char* ws = static_cast<char*>(workspace);

@@ -592,19 +592,19 @@ def paged_decode_attention_static_scratch(out: torch.Tensor, q: torch.Tensor, k_
     return out
 
 
-# Stream-K test controls (kv_debug_set keys), process-wide.
+# Test controls of the stream-K and shared-prefix kernels (kv_debug_set keys), process-wide.
 DEBUG_WAIT_LIMIT_NS = 1
 DEBUG_SKIP_TILE = 2
 DEBUG_DEFAULTS = {DEBUG_WAIT_LIMIT_NS: 0, DEBUG_SKIP_TILE: -1}
 
 
 def debug_set(key: int, value: int) -> None:
-    """Set one stream-K test control (see kv_debug_set)."""
+    """Set one test control (see kv_debug_set)."""
     check(lib().kv_debug_set(int(key), int(value)), "kv_debug_set")
 
 
 def debug_reset() -> None:
-    """Every stream-K control back to its default."""
+    """Every test control back to its default."""
     for key, value in DEBUG_DEFAULTS.items():
         debug_set(key, value)
 
