@@ -804,8 +804,8 @@ int kvstep_last_buffers(kvstep_t h, const int32_t** slot_mapping, const int32_t*
                         const int32_t** seq_lens, const int32_t** new_token_row);
 
 /* Test controls of the stream-K decode kernel (and, where it is said, the
- * shared-prefix kernel), process-wide, read at each later launch (no
- * counterpart on the pages).  Keys:
+ * shared-prefix and the tcgen05 prefill kernel), process-wide, read at each
+ * later launch (no counterpart on the pages).  Keys:
  *   KV_DEBUG_WAIT_LIMIT_NS: longest one bounded device wait may take before
  *     the kernel records KV_ERR_DEVICE_TIMEOUT and gives up (value <= 0
  *     restores the default, 1 s).
@@ -814,9 +814,9 @@ int kvstep_last_buffers(kvstep_t h, const int32_t** slot_mapping, const int32_t*
  *     runs out after the wait limit; the launch still ends, records
  *     KV_ERR_DEVICE_TIMEOUT, and its outputs are unspecified.  The
  *     shared-prefix kernel's first share of prefix units never loads its copy
- *     number `value` (K and V tiles in their order); its waits always take 1 s
- *     to run out.  value < 0: off.  For tests of the timeout path, which need
- *     no GPU fault.
+ *     number `value` (K and V tiles in their order), the prefill kernel's CTA 0
+ *     its K tile `value`; their waits always take 1 s to run out.  value < 0:
+ *     off.  For tests of the timeout path, which need no GPU fault.
  * KV_ERR_INVALID_ARG for an unknown key. */
 enum { KV_DEBUG_WAIT_LIMIT_NS = 1, KV_DEBUG_SKIP_TILE = 2 };
 int kv_debug_set(int key, int64_t value);

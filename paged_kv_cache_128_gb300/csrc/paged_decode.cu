@@ -1669,7 +1669,7 @@ uint64_t next_epoch() {
 }
 
 // Stream-K test controls (kv_debug_set), read at each launch; the
-// shared-prefix kernel reads skip_tile too.
+// shared-prefix and prefill kernels read skip_tile too.
 struct SkControls {
   std::atomic<int64_t> wait_limit_ns{static_cast<int64_t>(kWaitLimitNs)};
   std::atomic<int64_t> skip_tile{-1};

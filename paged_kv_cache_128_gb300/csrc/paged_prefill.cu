@@ -53,6 +53,7 @@ struct PrefillParams {
   int64_t num_tokens;  // rows of q and out
   int32_t hg_log2;     // tensor-core kernel: log2 of the query heads per row tile
   int32_t row_tiles;   // tensor-core kernel: row tiles per (sequence, head group) in the grid
+  int32_t test_skip;   // tensor-core kernel, test control (-1: off): CTA 0 never loads this K tile
 };
 
 // Byte offset of (key, dim) in a [kPfKeys][D] 16-bit tile: 128-byte slabs of
@@ -337,7 +338,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   uint64_t* bar_s = bar_vempty + VST;          // S written
   uint64_t* bar_p = bar_s + 1;                 // P written (every softmax thread arrives)
   uint64_t* bar_pv = bar_p + 1;                // P V done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_pv + 1);
+  uint64_t* bar_end = bar_pv + 1;              // after a wait ran out: all MMAs done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_end + 1);
 
   const int hg = 1 << p.hg_log2, tpt = kTcRows >> p.hg_log2;
   // 1-D grid over (head group, sequence, row tile), the row tile slowest and
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int nst = is_v ? VST : KST, st = j % nst;
     uint64_t* full = (is_v ? bar_vfull : bar_kfull) + st;
     if (j >= nst && !mbar_wait_bounded((is_v ? bar_vempty : bar_kempty) + st, ((j / nst) - 1) & 1)) return false;
+    if (!is_v && j == p.test_skip && blockIdx.x == 0) return true;
     const int k0 = j * kTcKeys, k1 = min(k0 + kTcKeys, nkeys);
     const int blk0 = k0 / bs, blk1 = (k1 + bs - 1) / bs;
     mbar_arrive_expect_tx(full, static_cast<uint32_t>((blk1 - blk0) * bs * D * 2));
@@ -414,6 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     mbar_init(bar_s, 1);
     mbar_init(bar_p, kTcSoftWarps * 32);
     mbar_init(bar_pv, 1);
+    mbar_init(bar_end, 1);
     fence_mbar_init();
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
@@ -433,13 +437,23 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (lane == 0) {
       // ---- TMA producer (Q and the first K tile are already issued)
       bool ok = load_ok;
-      for (int j = 0; j < ntiles && ok; ++j) {
+      int j = 0;
+      for (; j < ntiles && ok; ++j) {
         ok = load(j, true);
         if (ok && j + 1 < ntiles) ok = load(j + 1, false);
       }
-      // every stage's last S and P V have completed (no copy or commit in flight at exit)
-      for (int j = max(0, ntiles - KST); j < ntiles; ++j) mbar_wait_bounded(bar_kempty + (j % KST), (j / KST) & 1);
-      for (int j = max(0, ntiles - VST); j < ntiles; ++j) mbar_wait_bounded(bar_vempty + (j % VST), (j / VST) & 1);
+      // At exit no copy or commit is in flight: every stage's last S and P V
+      // have completed, or, where a wait ran out (the MMA lane may be gone), at
+      // least the copies have landed.
+      for (int i = max(0, ntiles - KST); i < ntiles && ok; ++i)
+        ok = mbar_wait_bounded(bar_kempty + (i % KST), (i / KST) & 1);
+      for (int i = max(0, ntiles - VST); i < ntiles && ok; ++i)
+        ok = mbar_wait_bounded(bar_vempty + (i % VST), (i / VST) & 1);
+      if (!ok) {  // j K tiles are armed, and j V tiles or one less
+        mbar_wait_bounded(bar_q, 0);
+        drain_fills(bar_kfull, j, KST, true);
+        drain_fills(bar_vfull, j, VST, true);
+      }
     }
   } else if (warp == kTcMmaWarp) {
     if (lane == 0) {
@@ -450,9 +464,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const uint32_t aQ = smem_u32(sm + Lay::kOffQ);
       for (int j = 0; j < ntiles && ok; ++j) {
         const int ks = j % KST, vs = j % VST;
-        if (!mbar_wait_bounded(bar_kfull + ks, (j / KST) & 1)) break;
+        ok = mbar_wait_bounded(bar_kfull + ks, (j / KST) & 1);
         // S overwrites P of the previous tile: its P V must be done
-        if (j > 0 && !mbar_wait_bounded(bar_pv, (j - 1) & 1)) break;
+        if (j > 0) ok = ok && mbar_wait_bounded(bar_pv, (j - 1) & 1);
+        if (!ok) break;
         tc::fence_after();
         const uint32_t kb = smem_u32(sm + Lay::kOffK + ks * Lay::kTile);
 #pragma unroll
@@ -462,9 +477,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         tc::commit(bar_s);
         tc::commit(bar_kempty + ks);
-        if (!mbar_wait_bounded(bar_vfull + vs, (j / VST) & 1)) break;
+        ok = mbar_wait_bounded(bar_vfull + vs, (j / VST) & 1);
         // P lands after the softmax warps have zeroed the last tile's V tail
-        if (!mbar_wait_bounded(bar_p, j & 1)) break;
+        ok = ok && mbar_wait_bounded(bar_p, j & 1);
+        if (!ok) break;
         tc::fence_after();
         const uint32_t vb = smem_u32(sm + Lay::kOffV + vs * Lay::kTile);
 #pragma unroll
@@ -475,6 +491,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         tc::commit(bar_pv);
         tc::commit(bar_vempty + vs);
+      }
+      if (!ok) {  // a wait ran out: what was issued ends before the tensor memory goes
+        tc::commit(bar_end);
+        mbar_wait_bounded(bar_end, 0);
       }
     }
   } else {
@@ -770,6 +790,7 @@ extern "C" int paged_prefill_attention(void* out, const void* q, const void* k_c
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.num_tokens = num_query_tokens;
+  p.test_skip = debug_skip_tile();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!tc_supported(block_size)) {
     const cudaError_t e = dtype == KV_DTYPE_F16 ? launch_prefill<__half>(p, head_dim, max_query_len, st)

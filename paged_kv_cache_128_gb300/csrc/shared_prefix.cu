@@ -79,7 +79,6 @@
 
 #include "common.cuh"
 #include "decode_tile.cuh"
-#include "stage_ring.h"
 #include "tcgen05.cuh"
 
 namespace pagedkv {
@@ -291,17 +290,6 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// The phases of a ring's last fills, each waited for (bounded): up to the
-// first wait that runs out, or all of them.  Not inlined, for the registers
-// of the loops before it (inlined: 64 sequences on 4096 tokens 29.9 us, not 29.0).
-__device__ __noinline__ bool sp_drain(uint64_t* bars, int armed, int stages, bool all) {
-  bool ok = true;
-  fills_in_flight(armed, stages, [&](int s, int parity) {
-    if ((ok || all) && !mbar_wait_bounded(bars + s, parity)) ok = false;
-  });
-  return ok;
-}
-
 // One warp's share of the rest line.
 template <typename T, int D, int NG>
 __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, const CUtensorMap& tmK,
@@ -447,7 +435,7 @@ __device__ __forceinline__ void rest_warp(const SpParams& p, const SpLine& ln, c
       reset_state(st);
     }
   }
-  if (!ok && lane == 0) sp_drain(full, issued, nst, true);  // a wait ran out: no copy in flight as the CTA ends
+  if (!ok && lane == 0) drain_fills(full, issued, nst, true);  // a wait ran out: no copy in flight as the CTA ends
 }
 
 // A CTA's share [x0, x1) of the prefix line.
@@ -542,7 +530,7 @@ __device__ __forceinline__ void prefix_cta(const SpParams& p, const SpLine& ln, 
     // completed, or, where a wait ran out (the MMA lane may be gone), at least
     // the copies have landed.
     if (lane == 0) {
-      if (!ok || !sp_drain(bar_empty, armed, nst, false)) sp_drain(bar_full, armed, nst, true);
+      if (!ok || !drain_fills(bar_empty, armed, nst, false)) drain_fills(bar_full, armed, nst, true);
     }
   } else if (warp == kSpMmaWarp) {
     if (lane == 0) {

@@ -592,7 +592,7 @@ def paged_decode_attention_static_scratch(out: torch.Tensor, q: torch.Tensor, k_
     return out
 
 
-# Test controls of the stream-K and shared-prefix kernels (kv_debug_set keys), process-wide.
+# Test controls of the stream-K, shared-prefix and prefill kernels (kv_debug_set keys), process-wide.
 DEBUG_WAIT_LIMIT_NS = 1
 DEBUG_SKIP_TILE = 2
 DEBUG_DEFAULTS = {DEBUG_WAIT_LIMIT_NS: 0, DEBUG_SKIP_TILE: -1}
