@@ -361,7 +361,8 @@ int paged_reshape_and_cache_fp8(const void* k, const void* v, void* k_cache, voi
  *   q, q_out: device [num_tokens, num_heads, head_dim], token t at
  *     + t * q_token_stride / q_out_token_stride elements, heads of one token
  *     contiguous.  q_out is q (same pointer and stride: rotated in place) or
- *     overlaps none of q, k, v.  num_heads 0: no queries (both may be NULL).
+ *     shares no byte with the rows of q, and none with those of k and v (else
+ *     KV_ERR_INVALID_ARG).  num_heads 0: no queries (both may be NULL).
  *   k, v, k_cache, v_cache, slot_mapping, strides, dtype: as for
  *     paged_reshape_and_cache.
  *   positions: device int32[num_tokens].

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "token_rows.h"
 
 namespace pagedkv {
 namespace {
@@ -352,9 +353,20 @@ int rope_impl(const RopeParams& in, int64_t num_tokens, int32_t interleaved, int
     return KV_ERR_INVALID_ARG;
   if (p.num_heads > 0 && (!p.q || !p.q_out)) return KV_ERR_INVALID_ARG;
   if (f8 && (!p.k_scales || !p.v_scales)) return KV_ERR_INVALID_ARG;
-  // rotating in place is token by token: the same rows, or none in common
-  if (p.num_heads > 0 && p.q_out == p.q && p.q_out_stride != p.q_stride) return KV_ERR_INVALID_ARG;
   const int64_t es = static_cast<int64_t>(dtype_bytes(dtype));
+  if (p.num_heads > 0) {
+    // rotating in place is token by token: the same rows, or none in common;
+    // k and v are read while q_out is written
+    if (p.q_out == p.q && p.q_out_stride != p.q_stride) return KV_ERR_INVALID_ARG;
+    auto rows = [&](const void* x, int64_t row, int64_t stride) {
+      return TokenRows{reinterpret_cast<uintptr_t>(x), row * es, stride * es};
+    };
+    const TokenRows qo = rows(p.q_out, q_row, p.q_out_stride);
+    if ((p.q_out != p.q && rows_overlap(qo, rows(p.q, q_row, p.q_stride), num_tokens)) ||
+        rows_overlap(qo, rows(p.k, kv_row, p.k_stride), num_tokens) ||
+        rows_overlap(qo, rows(p.v, kv_row, p.v_stride), num_tokens))
+      return KV_ERR_INVALID_ARG;
+  }
   const void* elems[] = {p.num_heads ? p.q : p.k, p.num_heads ? p.q_out : p.k, p.k, p.v};
   for (const void* x : elems)
     if (!rope_aligned(x, es)) return KV_ERR_INVALID_ARG;
