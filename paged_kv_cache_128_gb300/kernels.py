@@ -31,6 +31,16 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _call_workspace(stream: Optional[torch.cuda.Stream], alloc, *args) -> Optional[torch.Tensor]:
+    """A workspace for one call, from the memory of the stream that the call
+    runs on: another stream's memory may still be in use by earlier work
+    there, and may be handed out again there before the call is over."""
+    if stream is None:
+        return alloc(*args)
+    with torch.cuda.stream(stream):
+        return alloc(*args)
+
+
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise KVError(1, f"{name} must be a CUDA tensor")
@@ -245,7 +255,8 @@ def paged_decode_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
             or block_tables.shape[0] != B or seq_lens.numel() != B:
         raise KVError(1, "block_tables must be [B, max_blocks] and seq_lens [B], int32")
     if workspace is None:
-        workspace = alloc_workspace(decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype), q.device)
+        plan = decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype)
+        workspace = _call_workspace(stream, alloc_workspace, plan, q.device)
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     check(lib().paged_decode_attention_fp8(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
@@ -283,7 +294,8 @@ def paged_decode_step_fp8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
                 or t.stride(1) != d:
             raise KVError(1, "k and v must be [N, Hkv, D] with dense heads")
     if workspace is None:
-        workspace = alloc_workspace(decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype), q.device)
+        plan = decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype)
+        workspace = _call_workspace(stream, alloc_workspace, plan, q.device)
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     check(lib().paged_decode_step_fp8(out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                       slot_mapping.data_ptr(), n, k.stride(0), v.stride(0), new_token_row.data_ptr(),
@@ -434,7 +446,7 @@ def paged_decode_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     ws_ptr, ws_bytes = None, 0
     if workspace is None:
         plan = decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype, blocks_per_split)
-        workspace = alloc_workspace(plan, q.device)
+        workspace = _call_workspace(stream, alloc_workspace, plan, q.device)
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     check(lib().paged_decode_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -492,9 +504,7 @@ def paged_decode_attention_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_c
             or group_start.numel() != groups + 1:
         raise KVError(1, "block_tables [B, max_blocks], seq_lens [B], group_start [groups + 1], prefix_lens [groups]")
     if workspace is None:
-        workspace = shared_prefix_workspace(B, hq, hkv, d, bs, max_seq_len, dt, q.device)
-        if workspace is not None and stream is not None:
-            workspace.record_stream(stream)  # its memory is not handed out again while that stream may use it
+        workspace = _call_workspace(stream, shared_prefix_workspace, B, hq, hkv, d, bs, max_seq_len, dt, q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise KVError(1, "workspace must be contiguous on q's device")
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
@@ -542,7 +552,7 @@ def paged_decode_step(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     ws_ptr, ws_bytes = None, 0
     if workspace is None:
         plan = decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype)
-        workspace = alloc_workspace(plan, q.device)
+        workspace = _call_workspace(stream, alloc_workspace, plan, q.device)
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     check(lib().paged_decode_step(out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(),
