@@ -128,7 +128,7 @@ __device__ __forceinline__ void combine_and_store(const DecodeParams& p, const f
     const int qh = qh0 + g;
     if (single) {
       T* o = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.num_heads + qh) * D + d;
-      *o = DType<T>::from_float(den > 0.f ? num / den : 0.f);
+      *o = DType<T>::from_float(den == 0.f ? 0.f : num / den);  // a sum of NaN gives NaN
     } else {
       const int64_t row = (static_cast<int64_t>(b) * p.num_heads + qh) * p.num_splits + split;
       p.ws_o[row * D + d] = num;
@@ -152,6 +152,11 @@ __device__ __forceinline__ void store_zero_rows(const DecodeParams& p, int b, in
 // consecutive d are free of bank conflicts.
 template <int D>
 __host__ __device__ constexpr int merge_row() { return D + 4; }
+
+// The maximum that goes with a warp's sum where states are joined: the joins
+// skip a state whose maximum is -inf, but one whose scores were all NaN has a
+// sum of NaN that must reach the row.
+__device__ __forceinline__ float state_max(float m, float l) { return l != l ? 0.f : m; }
 
 // Reduce l across the lanes that share a head, then store this warp's
 // state: Os[cw][g][DP], Ms[cw][GP], Ls[cw][GP] (GP = 8 * NG, DP = D + 4).
@@ -182,7 +187,7 @@ __device__ __forceinline__ void store_state(WarpState<D, NG>& st, float* Os, flo
     for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        Ms[cw * GP + ng * 8 + lane * 2 + c] = st.m[ng][c];
+        Ms[cw * GP + ng * 8 + lane * 2 + c] = state_max(st.m[ng][c], st.l[ng][c]);
         Ls[cw * GP + ng * 8 + lane * 2 + c] = st.l[ng][c];
       }
   }
@@ -295,7 +300,7 @@ __device__ __forceinline__ void store_state_f8(WarpState<D, NG>& st, float* Os, 
     for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        Ms[cw * GP + ng * 8 + lane * 2 + c] = st.m[ng][c];
+        Ms[cw * GP + ng * 8 + lane * 2 + c] = state_max(st.m[ng][c], st.l[ng][c]);
         Ls[cw * GP + ng * 8 + lane * 2 + c] = st.l[ng][c];
       }
   }
@@ -1342,7 +1347,7 @@ decode_sk_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
     for (int i = 0; i < kOut; ++i) {
       const int idx = base + i * kStride;
-      if (idx < G * D) o[idx] = DType<T>::from_float(den[i] > 0.f ? num[i] / den[i] : 0.f);
+      if (idx < G * D) o[idx] = DType<T>::from_float(den[i] == 0.f ? 0.f : num[i] / den[i]);  // (NaN stays NaN)
     }
   }
 }
@@ -1558,7 +1563,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const Deco
 #pragma unroll
     for (int i = 0; i < DPL; ++i) Os[(warp * DP + lane + 32 * i) * GM + g] = acc[g][i];
     if (lane == 0) {
-      Ms[warp * GM + g] = mrun[g];
+      Ms[warp * GM + g] = state_max(mrun[g], lrun[g]);
       Ls[warp * GM + g] = lrun[g];
     }
   }
@@ -1580,7 +1585,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const Deco
     const int qh = kvh * G + g0 + g;
     if (nsplit_b == 1) {
       T* o = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.num_heads + qh) * D + d;
-      *o = DType<T>::from_float(den > 0.f ? num / den : 0.f);
+      *o = DType<T>::from_float(den == 0.f ? 0.f : num / den);  // a sum of NaN gives NaN
     } else {
       const int64_t r = (static_cast<int64_t>(b) * p.num_heads + qh) * p.num_splits + split;
       p.ws_o[r * D + d] = num;
