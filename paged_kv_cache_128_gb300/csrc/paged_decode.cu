@@ -1547,7 +1547,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const Deco
           for (int off = 16; off > 0; off >>= 1) sdot += __shfl_xor_sync(0xffffffffu, sdot, off);
           const float x = sdot * p.scale_log2;
           const float mn = fmaxf(mrun[g], x);
-          const float al = fast_exp2(mrun[g] - mn), pw = fast_exp2(x - mn);
+          const float mu = mn == -INFINITY ? 0.f : mn;  // no key of weight yet: e^(-inf) is 0
+          const float al = fast_exp2(mrun[g] - mu), pw = fast_exp2(x - mu);
           lrun[g] = lrun[g] * al + pw;
 #pragma unroll
           for (int i = 0; i < DPL; ++i) acc[g][i] = fmaf(acc[g][i], al, pw * vd[i]);

@@ -2,7 +2,7 @@
 that rounds its probabilities to 16 bits may be off by.
 
 The bound, from the arithmetic, for weights p_j and result o: the
-probabilities are rounded to the type (u: 2^-8 bf16, 2^-11 fp16, relative)
+probabilities are rounded to the type (u: 2^-8 bf16, 2^-11 fp16, 2^-24 fp32, relative)
 and summed as rounded, which moves the result by at most
 u sum_j p_j |V_j - o| / (1 - u); an fp16 probability below 2^-14 is rounded
 to a step of 2^-24, half of which, 2^-25, is its error against the row's
@@ -15,7 +15,7 @@ sums of the values and the joining of up to 1024 tiles' parts add
 
 import torch
 
-U = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+U = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 
 
 def attention64(q, k, v, scale, dtype, seen=None):
