@@ -601,8 +601,12 @@ int paged_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_heads, int3
  * paged_decode_attention.  fp16 and bf16 with head_dim 64 or 128, block_size
  * 16, 32, 64 or 128, at most 16 query heads per kv head and 4096 sequences
  * share prefixes (two launches, the prefixes on the 5th-generation tensor
- * cores); every other shape is one paged_decode_attention call.  fp32 accumulation and online softmax,
- * one rounding to dtype. */
+ * cores); every other shape is one paged_decode_attention call.  fp32
+ * accumulation and online softmax, probabilities rounded to dtype before they
+ * multiply V, one rounding of the result.
+ * What it saves is the prefix's repeated reads: in large batches whose shared
+ * part is less than about half of the lengths, or nothing,
+ * paged_decode_attention is as fast or up to 15 % faster. */
 int paged_decode_attention_shared_prefix(void* out, const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, const int32_t* seq_lens,
                                          const int32_t* group_start, const int32_t* prefix_lens, int32_t num_seqs,

@@ -31,8 +31,11 @@
 // tokens: one CTA per token walks all its heads.
 //
 // Measured on the device: 32768 tokens of 28 + 2 x 4 heads of 128, bf16: 96.7
-// us, 621 MB, 0.95 of the copy rate; 4581 of 32 + 2 x 8: 19.7 us (0.82), into
-// fp8 caches 23.1 us (0.64; 20.8 with a product in the place of the correctly
+// us, 621 MB, 0.95 of the copy rate; 4581 of 32 + 2 x 8: 19.8 us (0.82: 152
+// SMs of 12 CTAs hold 1824 tokens, so its 2.5 rounds take three), in float32
+// 34.2 us, 216 MB (0.94), into fp8 caches 23.4 us (0.64: a token's second round
+// of heads, where all its K and V rows lie, is loaded after the first is
+// stored and is half empty; 20.8 with a product in the place of the correctly
 // rounded divisions that the codes' definition asks for); 8 tokens: 2.0 us.
 
 #include <type_traits>

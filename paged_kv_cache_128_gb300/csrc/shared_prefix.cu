@@ -46,6 +46,11 @@
 //     maximum passes it by far; warps without a row of the unit skip the
 //     arithmetic.  They also lay a unit's Q into shared memory (any G: the
 //     rows are gathered) and write its results.
+// P is rounded to the cache's 16-bit type, on both lines and as in the other
+// attention kernels: the tensor cores take both operands of P V in one type.
+// The sum is taken over the rounded P, so a rounding moves a result by at most
+// u sum_j p_j |V_j - out| (u 2^-8 in bf16, 2^-11 in fp16).  Scores, sums, O and
+// the pieces are float32.
 // In a rest CTA each of warps 0-3 works by itself: its own ring of 16-token
 // tiles, its own copies, the decode kernels' mma.sync step (tokens in M, heads
 // in N) and its unit's whole softmax state in registers, so that a unit of a
@@ -58,13 +63,23 @@
 //   64 sequences, prefix 4096, rests up to 1024: 29 us, 75 MB (125 us);
 //   7 sequences, prefix 32768, rests up to 300: 34 us, 135 MB (128 us);
 //   256 sequences, prefix 8192, rests up to 512: 70 us, 131 MB, 35 GFLOP (740 us).
-// Some 13 us of each are there whatever the sizes: two launches, the lines
-// (2.5 us), Q and the first tiles, the last results and the merge; the
-// smallest call (4 sequences of 512) takes 9.6 us.  In the last case an SM of
-// the prefix line ends a tile every 0.53 us (1.2 PFLOP/s over all such SMs);
-// its tensor pipe is busy for 0.33 us of that (N 64: 48 clocks for 16 dims
-// where N 128 takes 64), the rest goes into the issuing lanes' turns, and
-// neither L2 (22 %) nor memory (27 %) is near its limit.
+// Time stamps in a copy of the kernel: the lines are built after 2.0 us (4
+// sequences) to 3.0 (256); the first scores are there after 3.9 to 7.4; the
+// last CTA's end is followed by 4 to 7 us of launch and merge.  So 8 of the
+// smallest call's 9.6 us (4 sequences of 512) and 12.5 to 13.5 us of the others
+// lie before the first tile and after the last.  A prefix CTA, two to an SM,
+// takes a tile in 1.16 us (256 sequences) to 1.4 (7, whose 16-token blocks take
+// four copies a tile).
+// Of the 70 us of 256 sequences, 6.6 go by before the first scores, 46 on 38 to
+// 42 tiles a CTA (0.8 PFLOP/s on the 113 SMs of the prefix line), 9 between the
+// median CTA's end (55 us, on both lines) and the last one's, and the rest after
+// it.  In those tiles an SM's tensor pipe is busy for 0.33 of 0.58 us (N 64: 48
+// clocks for 16 dims where N 128 takes 64); neither L2 (22 %) nor memory (27 %)
+// is near its limit.
+// Slower than paged_decode_attention where the rests are most of what is read:
+// 64 sequences, prefix 128, rests 1024 to 2048, 79 against 70 us; prefix 2048,
+// rests 2048 to 4096, 165 against 160; nothing shared, 512 tokens each, 28
+// against 27.
 // Slower in part of the cases, so not taken: one CTA per SM whose K and V
 // stages serve two row tiles (31 / 41 / 74 us: its one issuing lane sets the
 // pace); a fifth stage (30 / 37 / 71 us).

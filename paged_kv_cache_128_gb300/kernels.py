@@ -477,6 +477,8 @@ def paged_decode_attention_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_c
     group_start[g + 1] - 1`` share the blocks of their first
     ``prefix_lens[g]`` tokens (int32, ``[groups + 1]`` and ``[groups]``; see
     ``KVBlockManager.prefix_groups``), which are read once for the group.
+    In large batches whose shared part is less than about half of the
+    lengths, ``paged_decode_attention`` is as fast or up to 15 % faster.
     ``workspace``: ``shared_prefix_workspace(...)`` (allocated here if
     omitted)."""
     dev = q.get_device()
