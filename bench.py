@@ -125,7 +125,8 @@ def _code_only(text):
 def kernel_source_hash():
     """Hash of the decode kernels' source (comments and blank lines left out)."""
     h = hashlib.sha256()
-    for rel in ("paged_kv_cache_128_gb300/csrc/paged_decode.cu", "paged_kv_cache_128_gb300/csrc/common.cuh"):
+    for rel in ("paged_kv_cache_128_gb300/csrc/paged_decode.cu", "paged_kv_cache_128_gb300/csrc/decode_kernels.cuh",
+                "paged_kv_cache_128_gb300/csrc/decode_tile.cuh", "paged_kv_cache_128_gb300/csrc/common.cuh"):
         with open(os.path.join(ROOT, rel), encoding="utf-8") as f:
             h.update(_code_only(f.read()).encode())
     return h.hexdigest()[:16]

@@ -395,6 +395,36 @@ int paged_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const vo
                              int64_t q_out_token_stride, int64_t q_token_stride, int64_t k_token_stride,
                              int64_t v_token_stride, int dtype, void* stream);
 
+/* paged_rope_and_cache for tokens with a position on each of several axes
+ * (time, height and width of an image's or a film's tokens).  No passage, as
+ * for paged_rope_and_cache.  Pair i of a head turns by the angle i of its own
+ * axis' position: in the definition above, c and s come from the table's row
+ * positions[pair_axes[i]][t].
+ *   positions: device int32 [num_axes, num_tokens].
+ *   num_axes: 1..4.  pair_axes: HOST uint8[rot_dim / 2], each below num_axes,
+ *     read before the call returns; rot_dim at most 512.
+ * A token with any of its positions outside [0, max_positions) is recorded as
+ * KV_ERR_DEVICE_BOUNDS and skipped whole.  With num_axes 1 the result is
+ * paged_rope_and_cache's.  Other arguments and rules are those of
+ * paged_rope_and_cache. */
+int paged_rope_and_cache_axes(void* q_out, const void* q, const void* k, const void* v, const int32_t* positions,
+                              int32_t num_axes, const uint8_t* pair_axes, const float* cos_sin, void* k_cache,
+                              void* v_cache, const int32_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int64_t max_positions,
+                              int32_t interleaved, int32_t block_size, int64_t num_blocks,
+                              int64_t q_out_token_stride, int64_t q_token_stride, int64_t k_token_stride,
+                              int64_t v_token_stride, int dtype, void* stream);
+
+/* paged_rope_and_cache_axes into fp8 caches ("paged-attention-impl-detail",
+ * 实践建议 4), as paged_rope_and_cache_fp8 is to paged_rope_and_cache. */
+int paged_rope_and_cache_axes_fp8(void* q_out, const void* q, const void* k, const void* v, const int32_t* positions,
+                                  int32_t num_axes, const uint8_t* pair_axes, const float* cos_sin, void* k_cache,
+                                  void* v_cache, float* k_scales, float* v_scales, const int32_t* slot_mapping,
+                                  int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t rot_dim, int64_t max_positions, int32_t interleaved, int32_t block_size,
+                                  int64_t num_blocks, int64_t q_out_token_stride, int64_t q_token_stride,
+                                  int64_t k_token_stride, int64_t v_token_stride, int dtype, void* stream);
+
 /* paged_decode_attention over fp8 caches and their scales: K_j, V_j are the
  * dequantised rows (the fp8 KV cache of "paged-attention-impl-detail",
  * 实践建议 4, read by MiniPaged-Qwen §13's decode attention).  q and out are fp16 or bf16 (dtype); head_dim 128,
@@ -466,6 +496,66 @@ int paged_prefill_attention(void* out, const void* q, const void* k_cache, const
                             int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,
                             int32_t max_blocks_per_seq, int32_t max_query_len, float scale, int dtype,
                             void* stream);
+
+/* Attention under score rules.  No passage: the pages' attention weighs every
+ * key up to the query's own by its plain score; these calls are what models
+ * with capped scores, a distance bias in the place of positions, windows,
+ * packed documents or images need of the same cache.  For a query of head h at
+ * position i of a sequence of L tokens, and key j:
+ *   s_ij = scale q_i . K_j;  softcap c > 0: s_ij = c tanh(s_ij / c);
+ *   slopes: s_ij = s_ij - slopes[h] |i - j|;
+ *   seen: lo <= j < hi with lo = max(0, window > 0 ? i - window + 1 : 0,
+ *   key_begin) and hi = min(L, key_end, or i + 1 without key_end);
+ *   out = sum_{j seen} softmax_j(s_ij) V_j, and zeros where nothing is seen.
+ *   softcap: 0 (none) or a positive finite cap; scale / softcap and
+ *     softcap log2(e) must be float32 numbers.
+ *   slopes: device float32[num_heads], finite, or NULL.
+ *   window: 0 (all) or the number of keys seen up to and with the own one.
+ *   key_begin, key_end: device int32[query rows], any values, or NULL.
+ * A key that a query does not see takes no part in its row, whatever K holds
+ * there, and blocks that end before the first key seen are not looked up:
+ * their table entries may be anything, as when a window's old blocks have been
+ * released.  tanh is accurate to float32 (a polynomial for |s| <= c,
+ * exponentials beyond).
+ *
+ * paged_prefill_attention with rules: key_begin and key_end have one entry per
+ * row of q (positions in the row's sequence), so that a row can see its whole
+ * image or prefix (key_end past its own position) or only its document.
+ * Values: a row's weight on a key it does not see is 0, and V there is cleared
+ * where no row of a tile (128 / heads consecutive tokens; 64 in the mma.sync
+ * kernel) sees it; a NaN or infinity in the value of a key that another row of
+ * the tile sees can reach the row.  Other arguments and rules are those of
+ * paged_prefill_attention. */
+int paged_prefill_attention_rules(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, int64_t num_query_tokens, int32_t num_seqs,
+                                  int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                  int64_t num_blocks, int32_t max_blocks_per_seq, int32_t max_query_len, float scale,
+                                  float softcap, const float* slopes, int32_t window, const int32_t* key_begin,
+                                  const int32_t* key_end, int dtype, void* stream);
+
+/* paged_decode_attention with the score rules above (no passage, as there):
+ * the query is at position i = seq_lens[b] - 1, key_begin has one entry per
+ * sequence.  A sequence costs what the keys it sees cost.  The kernels and the
+ * workspace are those of paged_decode_attention for the same sizes
+ * (paged_decode_plan with blocks_per_split 0); other arguments and rules too. */
+int paged_decode_attention_rules(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs,
+                                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 int64_t num_blocks, int32_t max_blocks_per_seq, int64_t max_seq_len, float scale,
+                                 float softcap, const float* slopes, int32_t window, const int32_t* key_begin,
+                                 int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* paged_decode_attention_fp8 with the score rules above (the fp8 KV cache of
+ * "paged-attention-impl-detail", 实践建议 4); other arguments and rules are
+ * those of paged_decode_attention_fp8. */
+int paged_decode_attention_rules_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                     const int32_t* seq_lens, int32_t num_seqs, int32_t num_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                     int32_t max_blocks_per_seq, int64_t max_seq_len, float scale, float softcap,
+                                     const float* slopes, int32_t window, const int32_t* key_begin, int dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Copy-on-write block copies (kvbm_take_copies): for each i < n, block
  * dst[i] of every layer's K and V cache becomes a copy of block src[i]

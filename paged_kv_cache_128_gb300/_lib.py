@@ -91,6 +91,26 @@ SIGNATURES = {
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_int32,
                                          c_int32, c_int64, c_int32, c_int32, c_int64, c_int64, c_int64, c_int64,
                                          c_int64, c_int, c_void_p]),
+    "paged_rope_and_cache_axes": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_char_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32,
+                                          c_int64, c_int32, c_int32, c_int64, c_int64, c_int64, c_int64, c_int64, c_int,
+                                          c_void_p]),
+    "paged_rope_and_cache_axes_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_char_p,
+                                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                              c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int32, c_int64,
+                                              c_int64, c_int64, c_int64, c_int64, c_int, c_void_p]),
+    "paged_prefill_attention_rules": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_int64, c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32,
+                                              c_int32, c_float, c_float, c_void_p, c_int32, c_void_p, c_void_p, c_int,
+                                              c_void_p]),
+    "paged_decode_attention_rules": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
+                                             c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int64, c_float,
+                                             c_float, c_void_p, c_int32, c_void_p, c_int, c_void_p, c_size_t,
+                                             c_void_p]),
+    "paged_decode_attention_rules_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                 c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_int64,
+                                                 c_int32, c_int64, c_float, c_float, c_void_p, c_int32, c_void_p, c_int,
+                                                 c_void_p, c_size_t, c_void_p]),
     "paged_decode_attention_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                            c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32,
                                            c_int64, c_float, c_int, c_void_p, c_size_t, c_void_p]),

@@ -18,11 +18,13 @@ LIB_NAME = "libpagedkv.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 HEADERS = [os.path.join(ROOT, "include", "pagedkv.h"), os.path.join(CSRC, "common.cuh"),
            os.path.join(CSRC, "tcgen05.cuh"), os.path.join(CSRC, "decode_tile.cuh"),
-           os.path.join(CSRC, "stage_ring.h"), os.path.join(CSRC, "token_rows.h")]
+           os.path.join(CSRC, "decode_kernels.cuh"), os.path.join(CSRC, "prefill_common.cuh"),
+           os.path.join(CSRC, "score_rules.cuh"), os.path.join(CSRC, "stage_ring.h"),
+           os.path.join(CSRC, "token_rows.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CUDA_SOURCES = ["reshape_and_cache.cu", "paged_decode.cu", "paged_prefill.cu", "step_runner.cu",
-                "rope_and_cache.cu", "shared_prefix.cu"]
+                "rope_and_cache.cu", "shared_prefix.cu", "paged_decode_rules.cu", "paged_prefill_rules.cu"]
 CXX_SOURCES = ["block_manager.cpp"]
 
 

@@ -46,6 +46,9 @@ const char*& last_cuda_error_text();
 // KV_DEBUG_SKIP_TILE as set by kv_debug_set (-1: off).
 int32_t debug_skip_tile();
 
+// KV_DEBUG_WAIT_LIMIT_NS as set by kv_debug_set.
+int64_t debug_wait_limit_ns();
+
 // Map a CUDA result to a status, remembering the error text on failure.
 inline int cuda_status(cudaError_t e, const char* what = nullptr) {
   if (e == cudaSuccess) return KV_OK;

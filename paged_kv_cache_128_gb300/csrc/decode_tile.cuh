@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "score_rules.cuh"
 
 namespace pagedkv {
 
@@ -94,9 +95,9 @@ __device__ __forceinline__ void reset_state(WarpState<D, NG>& st) {
 // one tile held in shared memory at kt_a (K) and vt_a (V) as one step of the
 // online softmax: the score chains of the sub-tiles are interleaved, and
 // the running max, the rescale of the accumulator and l are updated once.
-template <typename T, int D, int PB, int NG, int NS>
+template <typename T, int D, int PB, int NG, int NS, typename R>
 __device__ __forceinline__ void consume_subtiles(WarpState<D, NG>& st, uint32_t kt_a, uint32_t vt_a, int tok0, int L,
-                                                 float sl2, int lane) {
+                                                 float sl2, int lane, const R& rules) {
   using M = Mma<T>;
   constexpr int KS = D / 16;
   // ldmatrix lane -> (row, column) of the 8x8 matrix it addresses
@@ -121,17 +122,17 @@ __device__ __forceinline__ void consume_subtiles(WarpState<D, NG>& st, uint32_t 
   uint32_t pb[NS][NG][2];
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng) {
-    // scores in the exp2 domain; rows past the sequence end are -inf
+    // scores in the exp2 domain; rows that are not seen (past the sequence end) are -inf
     float x[NS][4];
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int u = 0; u < NS; ++u) {
       const int t_lo = tok0 + u * 16 + (lane >> 2);
-      const bool in_lo = t_lo < L, in_hi = t_lo + 8 < L;
-      x[u][0] = in_lo ? sc[u][ng][0] * sl2 : -INFINITY;
-      x[u][1] = in_lo ? sc[u][ng][1] * sl2 : -INFINITY;
-      x[u][2] = in_hi ? sc[u][ng][2] * sl2 : -INFINITY;
-      x[u][3] = in_hi ? sc[u][ng][3] * sl2 : -INFINITY;
+      const bool in_lo = rule_sees(rules, t_lo, L), in_hi = rule_sees(rules, t_lo + 8, L);
+      x[u][0] = in_lo ? rule_score(rules, sc[u][ng][0], sl2, t_lo, ng, 0) : -INFINITY;
+      x[u][1] = in_lo ? rule_score(rules, sc[u][ng][1], sl2, t_lo, ng, 1) : -INFINITY;
+      x[u][2] = in_hi ? rule_score(rules, sc[u][ng][2], sl2, t_lo + 8, ng, 0) : -INFINITY;
+      x[u][3] = in_hi ? rule_score(rules, sc[u][ng][3], sl2, t_lo + 8, ng, 1) : -INFINITY;
       mx0 = fmaxf(mx0, fmaxf(x[u][0], x[u][2]));
       mx1 = fmaxf(mx1, fmaxf(x[u][1], x[u][3]));
     }
@@ -185,10 +186,20 @@ __device__ __forceinline__ void consume_subtiles(WarpState<D, NG>& st, uint32_t 
 // sequence end are skipped.
 // BS: tokens of the tile; PB: rows of each physical block in it (the tile's
 // layout, see swz).
-template <typename T, int D, int BS, int NG, int PB = BS>
+template <typename T, int D, int BS, int NG, int PB = BS, typename R = NoRules>
 __device__ __forceinline__ void consume_tile(WarpState<D, NG>& st, uint8_t* kt, uint8_t* vt, int tok0, int L,
-                                             float sl2, int lane) {
+                                             float sl2, int lane, const R& rules = R()) {
   const int valid = min(BS, L - tok0);
+  if constexpr (R::kOn) {
+    // and those before the first key that is seen (never loaded, some of them)
+    const int skipped = min(BS, rules.lo - tok0);
+    for (int c = lane; c < skipped * (D / 8); c += 32)
+      *reinterpret_cast<uint4*>(vt + swz<D, PB>(c / (D / 8), (c % (D / 8)) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+    if (skipped > 0 && valid >= BS) {
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+  }
   if (valid < BS) {
     // zero the V rows past the sequence end: P is 0 there, but 0 * NaN is not
     const int chunks = (BS - valid) * (D / 8);
@@ -201,11 +212,11 @@ __device__ __forceinline__ void consume_tile(WarpState<D, NG>& st, uint8_t* kt, 
   }
   const uint32_t kt_a = smem_u32(kt), vt_a = smem_u32(vt);
   if constexpr (BS == 32) {
-    if (valid > 16) consume_subtiles<T, D, PB, NG, 2>(st, kt_a, vt_a, tok0, L, sl2, lane);
-    else consume_subtiles<T, D, PB, NG, 1>(st, kt_a, vt_a, tok0, L, sl2, lane);
+    if (valid > 16) consume_subtiles<T, D, PB, NG, 2>(st, kt_a, vt_a, tok0, L, sl2, lane, rules);
+    else consume_subtiles<T, D, PB, NG, 1>(st, kt_a, vt_a, tok0, L, sl2, lane, rules);
   } else {
     static_assert(BS == 16, "tiles are 16 or 32 tokens");
-    consume_subtiles<T, D, PB, NG, 1>(st, kt_a, vt_a, tok0, L, sl2, lane);
+    consume_subtiles<T, D, PB, NG, 1>(st, kt_a, vt_a, tok0, L, sl2, lane, rules);
   }
 }
 

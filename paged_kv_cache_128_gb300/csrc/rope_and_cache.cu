@@ -12,6 +12,9 @@
 // the bit; it is rounded once more to the output type, or, for an fp8 cache,
 // quantised from float32 with no 16-bit rounding between ("paged-attention-
 // impl-detail", 实践建议 4: the row steps of the fp8 cache write).
+// With several axes (time, height, width of an image's or a film's tokens) a
+// token has one position per axis, and pair i is turned by the angle i of its
+// axis' position: row positions[axis(i)][t] of the table.
 // A slot of -1 marks a padded token: nothing is written for it
 // ("MiniPaged-Qwen" §11-§12, the cache write's rules).
 //
@@ -57,6 +60,8 @@ template <typename T, bool F8> struct RopeShape {
   static constexpr int kCtas = F8 || sizeof(T) == 4 ? 8 : 12;
 };
 
+constexpr int kRopeAxes = 4, kRopeAxisPairs = 256;
+
 struct RopeParams {
   void* q_out;
   const void* q;
@@ -72,7 +77,16 @@ struct RopeParams {
   int32_t num_heads, num_kv_heads, head_dim, rot_dim, block_size;
   int64_t max_positions, num_slots;
   int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+  // several axes (num_axes > 1): positions [num_axes][num_tokens], and the axis
+  // of each pair, two bits each from the lowest on
+  int64_t num_tokens;
+  int32_t num_axes;
+  uint64_t axis_of_pair[kRopeAxisPairs / 32];
 };
+
+__device__ __forceinline__ int rope_axis(const RopeParams& p, int pair) {
+  return static_cast<int>(p.axis_of_pair[pair >> 5] >> (2 * (pair & 31))) & 3;
+}
 
 // Position and slot of token t; false when the token is padded or out of
 // range (recorded by one thread of the CTA).
@@ -83,6 +97,15 @@ __device__ __forceinline__ bool rope_token(const RopeParams& p, int32_t pos, int
     return false;
   }
   return true;
+}
+
+// The same for a token with several positions; pos[a] of axis a.
+__device__ __forceinline__ bool rope_token_axes(const RopeParams& p, const int32_t (&pos)[kRopeAxes], int32_t slot,
+                                                bool reporter) {
+  bool in = true;
+#pragma unroll
+  for (int a = 0; a < kRopeAxes; ++a) in = in && (a >= p.num_axes || (pos[a] >= 0 && pos[a] < p.max_positions));
+  return rope_token(p, in ? 0 : -1, slot, reporter);
 }
 
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
@@ -134,7 +157,7 @@ __device__ __forceinline__ void rotate16(float (&x0)[8], float (&x1)[8], const f
 // One CTA per (token, part): the part's rounds of heads.  F8: K and V are
 // quantised, a head's D / 16 lanes (4, 8 or 16, so within one warp) taking
 // the row's largest magnitude by shuffles.
-template <typename T, bool INTER, bool F8>
+template <typename T, bool INTER, bool F8, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads, (RopeShape<T, F8>::kCtas))
 rope_cache_kernel(const RopeParams p, int threads) {
   constexpr int kUnits = RopeShape<T, F8>::kUnits;
@@ -151,7 +174,11 @@ rope_cache_kernel(const RopeParams p, int threads) {
   const int e1 = INTER || !turn ? e0 + 8 : e0 + half;
   const int first = blockIdx.y * (per * kUnits) + tid / lph, step = gridDim.y * (per * kUnits);
 
-  const int32_t slot = __ldg(p.slot_mapping + t), pos = __ldg(p.positions + t);
+  const int32_t slot = __ldg(p.slot_mapping + t);
+  int32_t pos[kRopeAxes];
+#pragma unroll
+  for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a)
+    if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES ? a * p.num_tokens : 0) + t);
   Run8<T> r[kUnits][2];
   auto load = [&](int h0) {
 #pragma unroll
@@ -170,16 +197,29 @@ rope_cache_kernel(const RopeParams p, int threads) {
   // the first heads' rows depend on neither position nor slot: their loads go
   // out beside those (a padded token's rows are read and dropped)
   load(first);
-  if (!rope_token(p, pos, slot, tid == 0 && blockIdx.y == 0)) return;
+  const bool reporter = tid == 0 && blockIdx.y == 0;
+  if (AXES ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) return;
   float c[8], s[8];
   if (turn) {
-    const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.rot_dim + col * 8;
+    // the lane's eight pairs; with several axes each axis' row gives those of
+    // them that are its own (an axis none of them has is not read)
+    const uint32_t mine = AXES ? static_cast<uint32_t>(p.axis_of_pair[col >> 2] >> (16 * (col & 3))) & 0xffffu : 0u;
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i));
-      c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
-      s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
+    for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a) {
+      uint32_t own[8], any = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any |= own[i] = !AXES || ((mine >> (2 * i)) & 3u) == static_cast<uint32_t>(a);
+      if (AXES && !any) continue;
+      const float* row = p.cos_sin + static_cast<int64_t>(pos[a]) * p.rot_dim + col * 8;
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
+        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i));
+        if (own[i]) c[i] = cv.x, s[i] = sv.x;
+        if (own[i + 1]) c[i + 1] = cv.y, s[i + 1] = sv.y;
+        if (own[i + 2]) c[i + 2] = cv.z, s[i + 2] = sv.z;
+        if (own[i + 3]) c[i + 3] = cv.w, s[i + 3] = sv.w;
+      }
     }
   }
   const int64_t blk = slot / p.block_size, off = slot % p.block_size;
@@ -253,7 +293,7 @@ rope_cache_kernel(const RopeParams p, int threads) {
 // Any head_dim, any even rot_dim, any alignment of the elements: one warp
 // per (token, head), lanes over the pairs and then over the values that pass
 // through.  F8 walks a K or V row twice (its largest magnitude, its codes).
-template <typename T, bool INTER, bool F8>
+template <typename T, bool INTER, bool F8, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_cache_any_kernel(const RopeParams p, int64_t num_tokens) {
   const int lane = threadIdx.x & 31;
   const int heads = p.num_heads + 2 * p.num_kv_heads, D = p.head_dim, half = p.rot_dim >> 1;
@@ -261,20 +301,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_any_kernel(const Rope
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5); w < total; w += nwarps) {
     const int64_t t = w / heads;
     const int h = static_cast<int>(w % heads);
-    const int32_t slot = __ldg(p.slot_mapping + t), pos = __ldg(p.positions + t);
-    if (!rope_token(p, pos, slot, lane == 0 && h == 0)) continue;
+    const int32_t slot = __ldg(p.slot_mapping + t);
+    int32_t pos[kRopeAxes];
+#pragma unroll
+    for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a)
+      if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES ? a * p.num_tokens : 0) + t);
+    const bool reporter = lane == 0 && h == 0;
+    if (AXES ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) continue;
     const bool is_q = h < p.num_heads, is_v = h >= p.num_heads + p.num_kv_heads;
     const int hk = h - p.num_heads - (is_v ? p.num_kv_heads : 0);
     const T* src = is_q ? static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * D
                         : static_cast<const T*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) +
                               static_cast<int64_t>(hk) * D;
-    const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.rot_dim;
+    auto row_of = [&](int i) {  // the table row of pair i
+      int32_t at = pos[0];
+      if constexpr (AXES) {
+        const int axis = rope_axis(p, i);
+#pragma unroll
+        for (int a = 1; a < kRopeAxes; ++a) at = axis == a ? pos[a] : at;
+      }
+      return p.cos_sin + static_cast<int64_t>(at) * p.rot_dim;
+    };
     const int turned = is_v ? 0 : p.rot_dim;
     // visit(e, y): every output value of the row once, pairs first
     auto walk = [&](auto visit) {
       for (int i = lane; i < turned / 2; i += 32) {
         const int ea = INTER ? 2 * i : i, eb = INTER ? 2 * i + 1 : i + half;
         float a = DType<T>::to_float(src[ea]), b = DType<T>::to_float(src[eb]);
+        const float* row = row_of(i);
         rotate_pair(a, b, __ldg(row + i), __ldg(row + half + i));
         visit(ea, a);
         visit(eb, b);
@@ -310,13 +364,13 @@ int rope_sms() {
   return sms > 0 ? sms : 1;
 }
 
-template <typename T, bool INTER, bool F8>
+template <typename T, bool INTER, bool F8, bool AXES>
 cudaError_t launch_rope(const RopeParams& p, int64_t n, bool vec, cudaStream_t st) {
   const int heads = p.num_heads + 2 * p.num_kv_heads;
   const int64_t sms = rope_sms();
   if (!vec) {
     const int64_t need = (n * heads + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    rope_cache_any_kernel<T, INTER, F8>
+    rope_cache_any_kernel<T, INTER, F8, AXES>
         <<<static_cast<unsigned>(need < sms * 64 ? need : sms * 64), kRopeThreads, 0, st>>>(p, n);
     return cudaGetLastError();
   }
@@ -326,16 +380,19 @@ cudaError_t launch_rope(const RopeParams& p, int64_t n, bool vec, cudaStream_t s
   const int rounds = (heads + threads / lph * kUnits - 1) / (threads / lph * kUnits);
   // all rounds side by side while the tokens alone leave SMs short of CTAs
   const int parts = n < sms * 8 ? (rounds < 65535 ? rounds : 65535) : 1;
-  rope_cache_kernel<T, INTER, F8><<<dim3(static_cast<unsigned>(n), parts), threads, 0, st>>>(p, threads);
+  rope_cache_kernel<T, INTER, F8, AXES><<<dim3(static_cast<unsigned>(n), parts), threads, 0, st>>>(p, threads);
   return cudaGetLastError();
 }
 
 template <typename T, bool F8>
 cudaError_t launch_rope_form(const RopeParams& p, int64_t n, bool vec, bool inter, cudaStream_t st) {
-  return inter ? launch_rope<T, true, F8>(p, n, vec, st) : launch_rope<T, false, F8>(p, n, vec, st);
+  // one axis: the single-position kernels, its row of positions being the only one
+  if (p.num_axes > 1)
+    return inter ? launch_rope<T, true, F8, true>(p, n, vec, st) : launch_rope<T, false, F8, true>(p, n, vec, st);
+  return inter ? launch_rope<T, true, F8, false>(p, n, vec, st) : launch_rope<T, false, F8, false>(p, n, vec, st);
 }
 
-// Checks shared by both entry points, then the launch.
+// Checks shared by the entry points, then the launch.
 int rope_impl(const RopeParams& in, int64_t num_tokens, int32_t interleaved, int64_t num_blocks, int dtype, bool f8,
               cudaStream_t st) {
   RopeParams p = in;
@@ -397,6 +454,19 @@ int rope_impl(const RopeParams& in, int64_t num_tokens, int32_t interleaved, int
   return cuda_status(e);
 }
 
+// The axes of a call with several positions per token, checked, into `p`.
+int rope_axes(RopeParams& p, int64_t num_tokens, int32_t num_axes, const uint8_t* pair_axes) {
+  if (num_axes < 1 || num_axes > kRopeAxes) return KV_ERR_INVALID_ARG;
+  if (p.rot_dim <= 0 || p.rot_dim % 2 != 0 || p.rot_dim / 2 > kRopeAxisPairs || !pair_axes) return KV_ERR_INVALID_ARG;
+  p.num_tokens = num_tokens;
+  p.num_axes = num_axes;
+  for (int i = 0; i < p.rot_dim / 2; ++i) {
+    if (pair_axes[i] >= num_axes) return KV_ERR_INVALID_ARG;
+    p.axis_of_pair[i >> 5] |= static_cast<uint64_t>(pair_axes[i]) << (2 * (i & 31));
+  }
+  return KV_OK;
+}
+
 }  // namespace
 }  // namespace pagedkv
 
@@ -428,6 +498,40 @@ extern "C" int paged_rope_and_cache_fp8(void* q_out, const void* q, const void* 
   const RopeParams p{q_out, q, k, v, positions, cos_sin, k_cache, v_cache, k_scales, v_scales, slot_mapping, num_heads,
                      num_kv_heads, head_dim, rot_dim, block_size, max_positions, 0, q_out_token_stride,
                      q_token_stride, k_token_stride, v_token_stride};
+  return rope_impl(p, num_tokens, interleaved, num_blocks, dtype, true, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int paged_rope_and_cache_axes(void* q_out, const void* q, const void* k, const void* v,
+                                         const int32_t* positions, int32_t num_axes, const uint8_t* pair_axes,
+                                         const float* cos_sin, void* k_cache, void* v_cache,
+                                         const int32_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                                         int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                                         int64_t max_positions, int32_t interleaved, int32_t block_size,
+                                         int64_t num_blocks, int64_t q_out_token_stride, int64_t q_token_stride,
+                                         int64_t k_token_stride, int64_t v_token_stride, int dtype, void* stream) {
+  if (dtype != KV_DTYPE_F32 && dtype != KV_DTYPE_F16 && dtype != KV_DTYPE_BF16) return KV_ERR_INVALID_ARG;
+  RopeParams p{q_out, q, k, v, positions, cos_sin, k_cache, v_cache, nullptr, nullptr, slot_mapping, num_heads,
+               num_kv_heads, head_dim, rot_dim, block_size, max_positions, 0, q_out_token_stride, q_token_stride,
+               k_token_stride, v_token_stride};
+  const int st = rope_axes(p, num_tokens, num_axes, pair_axes);
+  if (st != KV_OK) return st;
+  return rope_impl(p, num_tokens, interleaved, num_blocks, dtype, false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int paged_rope_and_cache_axes_fp8(
+    void* q_out, const void* q, const void* k, const void* v, const int32_t* positions, int32_t num_axes,
+    const uint8_t* pair_axes, const float* cos_sin, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+    const int32_t* slot_mapping, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t rot_dim, int64_t max_positions, int32_t interleaved, int32_t block_size, int64_t num_blocks,
+    int64_t q_out_token_stride, int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride, int dtype,
+    void* stream) {
+  if (dtype != KV_DTYPE_F16 && dtype != KV_DTYPE_BF16) return KV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KV_ERR_INVALID_ARG;
+  RopeParams p{q_out, q, k, v, positions, cos_sin, k_cache, v_cache, k_scales, v_scales, slot_mapping, num_heads,
+               num_kv_heads, head_dim, rot_dim, block_size, max_positions, 0, q_out_token_stride, q_token_stride,
+               k_token_stride, v_token_stride};
+  const int st = rope_axes(p, num_tokens, num_axes, pair_axes);
+  if (st != KV_OK) return st;
   return rope_impl(p, num_tokens, interleaved, num_blocks, dtype, true, static_cast<cudaStream_t>(stream));
 }
 

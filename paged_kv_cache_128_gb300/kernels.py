@@ -136,10 +136,10 @@ def _check_device(dev: int, tensors, names: str) -> None:
                           f"{n} is on cuda:{t.get_device()}, another tensor on cuda:{dev}")
 
 
-def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping):
-    """Checks shared by the two rotating cache writes; the sizes of the call:
+def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, pair_axes=None):
+    """Checks shared by the rotating cache writes; the sizes of the call:
     (N, Hq, Hkv, D, rot_dim, max_positions, bs, NB, token strides of q_out, q,
-    k and v)."""
+    k and v).  ``pair_axes``: several positions per token, ``[axes, N]``."""
     _check_device(k_cache.get_device(), (k, v, positions, cos_sin, k_cache, v_cache, slot_mapping),
                   "k v positions cos_sin k_cache v_cache slot_mapping")
     shape, dt = k.shape, k.dtype
@@ -148,7 +148,13 @@ def _rope_args(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mappin
         raise KVError(1, "caches must be contiguous [NB, BS, Hkv, D] of one shape")
     nb, bs, hkv, d = cache
     n = slot_mapping.numel()
-    if slot_mapping.dtype != torch.int32 or positions.dtype != torch.int32 or positions.numel() != n \
+    if pair_axes is not None:
+        if slot_mapping.dtype != torch.int32 or positions.dtype != torch.int32 or positions.dim() != 2 \
+                or positions.shape[1] != n or not slot_mapping.is_contiguous() or not positions.is_contiguous():
+            raise KVError(1, "slot_mapping [N] and positions [axes, N] must be contiguous int32")
+        if not isinstance(pair_axes, bytes) or 2 * len(pair_axes) != cos_sin.shape[-1]:
+            raise KVError(1, "pair_axes must be bytes, one axis for each of the rot_dim / 2 pairs")
+    elif slot_mapping.dtype != torch.int32 or positions.dtype != torch.int32 or positions.numel() != n \
             or not slot_mapping.is_contiguous() or not positions.is_contiguous():
         raise KVError(1, "slot_mapping and positions must be contiguous int32 of one length")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
@@ -235,6 +241,178 @@ def rope_and_cache_fp8(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
                                          bs, nb, so, sq, sk, sv, dtype_code(k.dtype), _stream_ptr(stream)),
           "paged_rope_and_cache_fp8")
     return q_out
+
+
+def rope_and_cache_axes(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor, pair_axes: bytes, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, slot_mapping: torch.Tensor, interleaved: bool = False,
+                        stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """``rope_and_cache`` for tokens with a position on each of up to four
+    axes (time, height, width): ``positions`` int32 ``[axes, N]``, and pair i
+    of a head turns by the angle i of ``positions[pair_axes[i]]``.
+    ``pair_axes``: bytes, one axis per pair -- ``bytes([0] * 16 + [1] * 24 +
+    [2] * 24)`` for three sections, or the axes in turn."""
+    n, hq, hkv, d, rot, rows, bs, nb, so, sq, sk, sv = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache,
+                                                                  v_cache, slot_mapping, pair_axes)
+    dt = k.dtype
+    if k_cache.dtype != dt or v_cache.dtype != dt:
+        raise KVError(1, "k, v and the caches must share one dtype")
+    if k_cache.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(k_cache.device):
+            return rope_and_cache_axes(q_out, q, k, v, positions, pair_axes, cos_sin, k_cache, v_cache, slot_mapping,
+                                       interleaved, stream)
+    check(lib().paged_rope_and_cache_axes(q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(),
+                                          v.data_ptr(), positions.data_ptr(), positions.shape[0], pair_axes,
+                                          cos_sin.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                          slot_mapping.data_ptr(), n, hq, hkv, d, rot, rows, 1 if interleaved else 0,
+                                          bs, nb, so, sq, sk, sv, dtype_code(dt), _stream_ptr(stream)),
+          "paged_rope_and_cache_axes")
+    return q_out
+
+
+def rope_and_cache_axes_fp8(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor,
+                            v: torch.Tensor, positions: torch.Tensor, pair_axes: bytes, cos_sin: torch.Tensor,
+                            k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                            v_scales: torch.Tensor, slot_mapping: torch.Tensor, interleaved: bool = False,
+                            stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """``rope_and_cache_axes`` into fp8 caches, as ``rope_and_cache_fp8`` is
+    to ``rope_and_cache``."""
+    n, hq, hkv, d, rot, rows, bs, nb, so, sq, sk, sv = _rope_args(q_out, q, k, v, positions, cos_sin, k_cache,
+                                                                  v_cache, slot_mapping, pair_axes)
+    _check_device(k_cache.get_device(), (k_scales, v_scales), "k_scales v_scales")
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_scales.dtype != torch.float32 \
+            or v_scales.dtype != torch.float32:
+        raise KVError(1, "fp8 caches are uint8 codes with float32 scales")
+    if k_scales.shape != (nb, hkv, bs) or v_scales.shape != (nb, hkv, bs) or not k_scales.is_contiguous() \
+            or not v_scales.is_contiguous():
+        raise KVError(1, "scales must be contiguous [NB, Hkv, BS]")
+    if k_cache.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(k_cache.device):
+            return rope_and_cache_axes_fp8(q_out, q, k, v, positions, pair_axes, cos_sin, k_cache, v_cache, k_scales,
+                                           v_scales, slot_mapping, interleaved, stream)
+    check(lib().paged_rope_and_cache_axes_fp8(
+        q_out.data_ptr() if hq else None, q.data_ptr() if hq else None, k.data_ptr(), v.data_ptr(),
+        positions.data_ptr(), positions.shape[0], pair_axes, cos_sin.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, rot,
+        rows, 1 if interleaved else 0, bs, nb, so, sq, sk, sv, dtype_code(k.dtype), _stream_ptr(stream)),
+        "paged_rope_and_cache_axes_fp8")
+    return q_out
+
+
+def _rules_args(dev: int, hq: int, rows: int, softcap: float, slopes, window: int, key_begin, key_end=None):
+    """Checks of the score rules' tensors; the rules as the C calls take them:
+    (softcap, slopes, window, key_begin, key_end), pointers or None."""
+    if slopes is not None:
+        if slopes.get_device() != dev or slopes.dtype != torch.float32 or slopes.numel() != hq \
+                or not slopes.is_contiguous():
+            raise KVError(1, "slopes must be contiguous float32 [Hq] on q's device")
+        slopes = slopes.data_ptr()
+    if key_begin is not None:
+        if key_begin.get_device() != dev or key_begin.dtype != torch.int32 or key_begin.numel() != rows \
+                or not key_begin.is_contiguous():
+            raise KVError(1, "key_begin must be contiguous int32, one per query row, on q's device")
+        key_begin = key_begin.data_ptr()
+    if key_end is not None:
+        if key_end.get_device() != dev or key_end.dtype != torch.int32 or key_end.numel() != rows \
+                or not key_end.is_contiguous():
+            raise KVError(1, "key_end must be contiguous int32, one per query row, on q's device")
+        key_end = key_end.data_ptr()
+    if not 0 <= window < 2 ** 31:
+        raise KVError(1, "window must be 0 (all) or a number of keys")
+    return float(softcap), slopes, window, key_begin, key_end
+
+
+def _rules_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, cache_dtype):
+    """Checks shared by the two decode calls with rules; (B, Hq, D, NB, bs,
+    Hkv, max_blocks)."""
+    _check_device(q.get_device(), (q, out, k_cache, v_cache, block_tables, seq_lens),
+                  "q out k_cache v_cache block_tables seq_lens")
+    shape, cache, dt = q.shape, k_cache.shape, q.dtype
+    if len(shape) != 3 or len(cache) != 4:
+        raise KVError(1, "q [B, Hq, D], caches [NB, BS, Hkv, D]")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise KVError(1, "q, out and caches must be contiguous")
+    if cache[3] != shape[2] or out.shape != shape or v_cache.shape != cache or out.dtype != dt \
+            or k_cache.dtype != cache_dtype or v_cache.dtype != cache_dtype:
+        raise KVError(1, "shape or dtype mismatch")
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or not block_tables.is_contiguous() \
+            or not seq_lens.is_contiguous() or block_tables.dim() != 2 or block_tables.shape[0] != shape[0] \
+            or seq_lens.numel() != shape[0]:
+        raise KVError(1, "block_tables [B, max_blocks] and seq_lens [B] must be contiguous int32")
+    return shape[0], shape[1], shape[2], cache[0], cache[1], cache[2], block_tables.shape[1]
+
+
+def _decode_workspace(workspace, stream, dev, B, hq, hkv, d, bs, max_seq_len, q):
+    """(pointer, bytes) of a decode call's workspace and the tensor that holds
+    it, allocated on the call's stream if None was given."""
+    if workspace is None:
+        plan = decode_plan(B, hq, hkv, d, bs, max_seq_len, q.dtype)
+        workspace = _call_workspace(stream, alloc_workspace, plan, q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise KVError(1, "workspace must be contiguous on q's device")
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def paged_decode_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, max_seq_len: int,
+                                 *, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                 key_begin: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``paged_decode_attention`` under score rules.  Key j of a sequence of L
+    tokens (the query's position is i = L - 1) scores ``s = scale q.k_j``,
+    capped to ``softcap * tanh(s / softcap)`` if ``softcap`` > 0, less
+    ``slopes[h] * (i - j)`` (float32 ``[Hq]``), and is seen if it is among the
+    last ``window`` keys (0: all) and ``j >= key_begin[b]`` (int32 ``[B]``).
+    A sequence that sees no key gets zeros.  Blocks that end before the first
+    key seen are not looked up.  ``workspace``: as for
+    ``paged_decode_attention``."""
+    dev = q.get_device()
+    B, hq, d, nb, bs, hkv, width = _rules_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, q.dtype)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return paged_decode_attention_rules(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len,
+                                                softcap=softcap, slopes=slopes, window=window, key_begin=key_begin,
+                                                workspace=workspace, stream=stream)
+    cap, sl, win, begin, _ = _rules_args(dev, hq, B, softcap, slopes, window, key_begin)
+    ws_ptr, ws_bytes, workspace = _decode_workspace(workspace, stream, dev, B, hq, hkv, d, bs, max_seq_len, q)
+    check(lib().paged_decode_attention_rules(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), B, hq, hkv, d, bs, nb, width, max_seq_len, float(scale), cap, sl, win, begin,
+        dtype_code(q.dtype), ws_ptr, ws_bytes, _stream_ptr(stream)), "paged_decode_attention_rules")
+    return out
+
+
+def paged_decode_attention_rules_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                     k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                     seq_lens: torch.Tensor, scale: float, max_seq_len: int, *, softcap: float = 0.0,
+                                     slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                     key_begin: Optional[torch.Tensor] = None,
+                                     workspace: Optional[torch.Tensor] = None,
+                                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``paged_decode_attention_rules`` over fp8 (E4M3) caches with per-token
+    scales (``[NB, Hkv, BS]``); q and out fp16/bf16."""
+    dev = q.get_device()
+    B, hq, d, nb, bs, hkv, width = _rules_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, torch.uint8)
+    _check_device(dev, (k_scales, v_scales), "k_scales v_scales")
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != (nb, hkv, bs) \
+            or v_scales.shape != (nb, hkv, bs) or not k_scales.is_contiguous() or not v_scales.is_contiguous():
+        raise KVError(1, "scales must be contiguous float32 [NB, Hkv, BS]")
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return paged_decode_attention_rules_fp8(
+                out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, scale, max_seq_len,
+                softcap=softcap, slopes=slopes, window=window, key_begin=key_begin, workspace=workspace,
+                stream=stream)
+    cap, sl, win, begin, _ = _rules_args(dev, hq, B, softcap, slopes, window, key_begin)
+    ws_ptr, ws_bytes, workspace = _decode_workspace(workspace, stream, dev, B, hq, hkv, d, bs, max_seq_len, q)
+    check(lib().paged_decode_attention_rules_fp8(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), B, hq, hkv, d, bs, nb, width, max_seq_len,
+        float(scale), cap, sl, win, begin, dtype_code(q.dtype), ws_ptr, ws_bytes, _stream_ptr(stream)),
+        "paged_decode_attention_rules_fp8")
+    return out
 
 
 def paged_decode_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -333,6 +511,55 @@ def paged_prefill_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
                                         block_tables.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), T,
                                         B, hq, hkv, d, bs, nb, block_tables.shape[1], max_query_len, float(scale),
                                         dtype_code(q.dtype), _stream_ptr(stream)), "paged_prefill_attention")
+    return out
+
+
+def paged_prefill_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                                  scale: float, max_query_len: int, *, softcap: float = 0.0,
+                                  slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                  key_begin: Optional[torch.Tensor] = None, key_end: Optional[torch.Tensor] = None,
+                                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``paged_prefill_attention`` under score rules.  Row r of q, at position
+    i of a sequence of L tokens, gives key j the score ``s = scale q.k_j``,
+    capped to ``softcap * tanh(s / softcap)`` if ``softcap`` > 0, less
+    ``slopes[h] * |i - j|`` (float32 ``[Hq]``), and sees it if
+    ``lo <= j < hi``: lo the larger of ``i - window + 1`` (``window`` > 0) and
+    ``key_begin[r]``, hi the smaller of L and ``key_end[r]`` (int32 ``[T]``,
+    positions in the row's sequence), or i + 1 without ``key_end``.  A
+    ``key_end`` past the row's own position lets it see ahead (a prefix, an
+    image), ``key_begin`` the start of its document.  A row that sees no key
+    gets zeros.  Blocks that end before the first key a tile of rows sees are
+    not looked up."""
+    dev = q.get_device()
+    _check_device(dev, (q, out, k_cache, v_cache, block_tables, seq_lens, query_start_loc),
+                  "q out k_cache v_cache block_tables seq_lens query_start_loc")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise KVError(1, "q [T, Hq, D], caches [NB, BS, Hkv, D]")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise KVError(1, "q, out and caches must be contiguous")
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, d2 = q.shape
+    B = seq_lens.numel()
+    if d2 != d or out.shape != q.shape or out.dtype != q.dtype or k_cache.dtype != q.dtype \
+            or v_cache.shape != k_cache.shape or v_cache.dtype != q.dtype:
+        raise KVError(1, "shape or dtype mismatch")
+    for t in (block_tables, seq_lens, query_start_loc):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise KVError(1, "block_tables, seq_lens and query_start_loc must be contiguous int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or query_start_loc.numel() != B + 1:
+        raise KVError(1, "block_tables [B, max_blocks], seq_lens [B], query_start_loc [B + 1]")
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return paged_prefill_attention_rules(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                                                 scale, max_query_len, softcap=softcap, slopes=slopes, window=window,
+                                                 key_begin=key_begin, key_end=key_end, stream=stream)
+    cap, sl, win, begin, end = _rules_args(dev, hq, T, softcap, slopes, window, key_begin, key_end)
+    check(lib().paged_prefill_attention_rules(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), T, B, hq, hkv, d, bs, nb, block_tables.shape[1],
+        max_query_len, float(scale), cap, sl, win, begin, end, dtype_code(q.dtype), _stream_ptr(stream)),
+        "paged_prefill_attention_rules")
     return out
 
 
