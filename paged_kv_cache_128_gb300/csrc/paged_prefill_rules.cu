@@ -2,7 +2,670 @@
 // scores, a bias that falls with the distance, windows, documents and spans
 // seen both ways, each query row over its own interval of keys.
 
+#include <algorithm>
+#include <type_traits>
+
 #include "prefill_common.cuh"
+
+namespace pagedkv {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Tensor-core (tcgen05) kernel under rules, for block sizes that divide 128
+// and are multiples of 16.
+//
+// Persistent CTAs, one per SM, walk items (head group, sequence, pair of row
+// tiles).  An item is two 128-row query tiles over one stream of 128-key tiles:
+// each K and V tile is loaded once for both, and one tile's softmax runs while
+// the tensor cores work for the other.  Rows are packed as in the plain
+// kernel: HG query heads of one kv head (the largest power of two dividing the
+// group, at most 8) times 128 / HG tokens.
+//
+// Each row sees an interval of keys, so a query tile needs the key tiles from
+// the smallest first key of its rows to their largest end; what neither tile
+// of the pair needs is not loaded.  The key tiles are walked from the last to
+// the first: under a falling bias, and in causal attention, a row's largest
+// scores then tend to come first, and the softmax reference, which moves only
+// when a score exceeds it by 2^8, stays where it is.
+//
+// Tensor memory (512 columns): S of the two tiles at 0 and 128 (P, two keys to
+// a column, over the upper half of its S), O at 256 and 256 + D.
+//   warp 9, scheduler and TMA producer: works out an item's ranges, hands them
+//     to the others through a two-deep ring in shared memory, and loads Q and
+//     the K and V tiles (one box per block and 64-dim slab, a lane each) into a
+//     ring of tile slots, running ahead into the next item;
+//   warp 8: one lane issues, for each key tile and for the two query tiles in
+//     turn, O += P V of the previous key tile and S = Q K^T of this one;
+//   warps 0-3 and 4-7: the softmax of the first and second query tile, a row
+//     per thread, as in the plain kernel.
+// V rows that lie in no row's interval are cleared before P V reads them.
+// ---------------------------------------------------------------------------
+constexpr int kRlSoftWarps = 4;  // per query tile
+constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1;
+constexpr int kRlThreads = 32 * (kRlTmaWarp + 1);
+constexpr uint32_t kRlCols = 512;
+
+template <int D>
+struct RlLayout {
+  static constexpr int kRing = D == 64 ? 8 : 5;      // K and V tile slots
+  static constexpr int kSlab = kTcRows * 128;        // one 64-column slab of 128 rows
+  static constexpr int kTile = (D / 64) * kSlab;     // a Q, K or V tile
+  static constexpr int kOffRing = 2 * kTile;         // after the two Q tiles
+  static constexpr int kOffBar = kOffRing + kRing * kTile;
+  static constexpr int kBytes = kOffBar + 512;
+  static constexpr int kSmem = kBytes + 1024;        // slack for 1024-byte alignment
+};
+
+// An item as the scheduler hands it on.
+struct RlItem {
+  int seq;          // -1: no more items
+  int q_row, n;     // first row of the sequence's chunk in q, its tokens
+  int ctx, len;     // positions before the chunk, and in all
+  int tok0, head0;  // first chunk token of the pair, first head of the group
+  int key_lo, key_hi;          // keys that some row of the pair sees
+  int tile_lo[2], tile_hi[2];  // key tiles of each query tile (none: equal)
+  int ring0;                   // ring position of the item's first K tile
+};
+
+__device__ __forceinline__ bool rl_needs(const RlItem& it, int q, int kt) {
+  return kt >= it.tile_lo[q] && kt < it.tile_hi[q];
+}
+
+// The polynomial of the cap for packed pairs: tanh(z) = z P(z^2) for |z| <= 1,
+// P of degree 5, within 6e-7 of it (the fit of soft_cap's, two terms shorter:
+// rounding the weights to 16 bits leaves 5e-4 and more).
+struct RlCap {
+  uint64_t arg, c[6];  // cap_arg and the coefficients times scale_log2
+  __device__ __forceinline__ RlCap(float cap_arg, float scale_log2) {
+    constexpr float k[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
+                            -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
+    arg = tc::f2(cap_arg, cap_arg);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c[i] = tc::f2(k[i] * scale_log2, k[i] * scale_log2);
+  }
+};
+
+template <typename T, int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kRlThreads, 1)
+    prefill_rules_kernel(const RulesPrefillParams p, const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+  using Lay = RlLayout<D>;
+  constexpr int kSlabs = D / 64, kRing = Lay::kRing;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t rl_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rl_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(sm + Lay::kOffBar);  // [kRing] tile landed
+  uint64_t* bar_empty = bar_full + kRing;       // [kRing] tile read
+  uint64_t* bar_qfull = bar_empty + kRing;      // Q landed
+  uint64_t* bar_qempty = bar_qfull + 1;         // the item's last S done
+  uint64_t* bar_s = bar_qempty + 1;             // [2] S written
+  uint64_t* bar_p = bar_s + 2;                  // [2] P written (one arrival per softmax warp)
+  uint64_t* bar_pv = bar_p + 2;                 // [2] P V done
+  uint64_t* bar_o = bar_pv + 2;                 // [2] O read (one arrival per softmax warp)
+  uint64_t* bar_item = bar_o + 2;               // [2] item slot filled
+  uint64_t* bar_free = bar_item + 2;            // [2] item slot read (MMA lane and every softmax warp)
+  uint64_t* bar_end = bar_free + 2;             // after a wait ran out: all MMAs done
+  RlItem* items = reinterpret_cast<RlItem*>(bar_end + 1);  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
+  static_assert((2 * kRing + 15) * 8 + 2 * sizeof(RlItem) + 4 <= 512, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hg = 1 << p.hg_log2, tpt = kTcRows >> p.hg_log2;  // heads and tokens of a row tile
+  const int bs = p.block_size;
+
+  if (warp == kRlTmaWarp && lane == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar_full + i, 1);
+      mbar_init(bar_empty + i, 1);
+    }
+    mbar_init(bar_qfull, 1);
+    mbar_init(bar_qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + i, 1);
+      mbar_init(bar_p + i, kRlSoftWarps);
+      mbar_init(bar_pv + i, 1);
+      mbar_init(bar_o + i, kRlSoftWarps);
+      mbar_init(bar_item + i, 1);
+      mbar_init(bar_free + i, 1 + 2 * kRlSoftWarps);
+    }
+    mbar_init(bar_end, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == kRlMmaWarp) tc::alloc(tmem_slot, kRlCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kRlTmaWarp) {
+    // ---- scheduler and TMA producer (the whole warp)
+    const int ngroups = p.num_heads >> p.hg_log2;
+    const int64_t total = static_cast<int64_t>(ngroups) * p.num_seqs * p.row_tiles;
+    int ring = 0, armed = 0, handed = 0, q_loads = 0, k_tiles = 0;
+    bool ok = true;
+    // a wait by lane 0 for the whole warp
+    auto wait = [&](uint64_t* bar, int parity) {
+      int w = 1;
+      if (lane == 0) w = mbar_wait_bounded(bar, parity);
+      ok = __shfl_sync(0xffffffffu, w, 0) != 0;
+      return ok;
+    };
+    auto hand_on = [&](const RlItem& it) {
+      const int slot = handed & 1;
+      if (handed >= 2 && !wait(bar_free + slot, ((handed >> 1) - 1) & 1)) return;
+      if (lane == 0) {
+        items[slot] = it;
+        mbar_arrive(bar_item + slot);
+      }
+      ++handed;
+    };
+    // Items come in order of falling length (row tiles counted down); every
+    // other round of CTAs takes them in reverse, so that the sums even out.
+    for (int64_t round = 0; round * gridDim.x < total && ok; ++round) {
+      const int64_t x = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (x >= total) continue;
+      const int gi = static_cast<int>(x % ngroups);
+      const int b = static_cast<int>((x / ngroups) % p.num_seqs);
+      const int pair = p.row_tiles - 1 - static_cast<int>(x / ngroups / p.num_seqs);
+      RlItem it;
+      it.seq = b;
+      it.q_row = __ldg(p.query_start + b);
+      it.n = __ldg(p.query_start + b + 1) - it.q_row;
+      it.tok0 = pair * 2 * tpt;
+      it.head0 = gi * hg;
+      // rows past the grid's reach (a chunk longer than max_query_len) would be
+      // left uncomputed: the sequence's last pair reports it
+      if (pair == p.row_tiles - 1 && gi == 0 && lane == 0 && it.n > p.row_tiles * 2 * static_cast<int64_t>(tpt))
+        record_error(KV_ERR_DEVICE_BOUNDS);
+      if (it.n <= 0 || it.tok0 >= it.n) continue;
+      it.len = __ldg(p.seq_lens + b);
+      const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+      // the chunk must lie inside its sequence and in q, the sequence in its table row
+      if (it.len < it.n || it.q_row < 0 || it.q_row + static_cast<int64_t>(it.n) > p.num_tokens) {
+        if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
+        continue;
+      }
+      if (it.len > cap) {
+        if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
+        it.len = static_cast<int>(cap);
+        if (it.len < it.n) continue;
+      }
+      it.ctx = it.len - it.n;
+      it.key_lo = INT32_MAX;
+      it.key_hi = 0;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
+        int lo = INT32_MAX, hi = 0;
+        if (p.rules.key_begin || p.rules.key_end) {
+          for (int t = t0 + lane; t < t1; t += 32) {
+            const KeySpan s = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, it.ctx + t, it.len);
+            if (s.lo < s.hi) {
+              lo = min(lo, s.lo);
+              hi = max(hi, s.hi);
+            }
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+        } else if (t0 < t1) {  // a window's ends move with the row
+          lo = keys_seen(p.rules, 0, it.ctx + t0, it.len).lo;
+          hi = keys_seen(p.rules, 0, it.ctx + t1 - 1, it.len).hi;
+        }
+        it.tile_lo[q] = lo < hi ? lo / kTcKeys : 0;
+        it.tile_hi[q] = lo < hi ? (hi + kTcKeys - 1) / kTcKeys : 0;
+        if (lo < hi) {
+          it.key_lo = min(it.key_lo, lo);
+          it.key_hi = max(it.key_hi, hi);
+        }
+      }
+      it.ring0 = ring;
+      hand_on(it);
+      if (!ok || it.key_lo >= it.key_hi) continue;
+      const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+      const int kvh = it.head0 / p.group;
+      // This lane's copy of a tile: slab lane % kSlabs of its block lane /
+      // kSlabs; a tile has the blocks that hold keys key_lo .. key_hi - 1.
+      const int my_blk = lane / kSlabs, my_slab = lane % kSlabs;
+      auto entry = [&](int kt) {  // table entry of this lane's block in tile kt (-1: none)
+        const int blk = kt * (kTcKeys / bs) + my_blk;
+        const bool in = my_blk < kTcKeys / bs && (blk + 1) * static_cast<int64_t>(bs) > it.key_lo &&
+                        static_cast<int64_t>(blk) * bs < it.key_hi;
+        int e = -1;
+        if (in) {
+          e = __ldg(table + blk);
+          if (e < 0 || e >= p.num_blocks) {
+            record_error(KV_ERR_DEVICE_BOUNDS);
+            e = 0;
+          }
+        }
+        return e;
+      };
+      auto load = [&](int kt, int e, bool is_v) {
+        const int slot = ring % kRing;
+        if (ring >= kRing && !wait(bar_empty + slot, ((ring / kRing) - 1) & 1)) return;
+        const bool skip = !is_v && p.test_skip >= 0 && blockIdx.x == 0 && k_tiles == p.test_skip;
+        if (!is_v) ++k_tiles;
+        if (skip) {
+          ok = false;  // test control: this tile never lands, and none after it
+          return;
+        }
+        const int copies = __popc(__ballot_sync(0xffffffffu, e >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(bar_full + slot, static_cast<uint32_t>(copies * bs * 128));
+        __syncwarp();
+        if (e >= 0)
+          tma_load_3d(sm + Lay::kOffRing + slot * Lay::kTile + my_slab * Lay::kSlab + my_blk * bs * 128,
+                      is_v ? &tmV : &tmK, bar_full + slot, my_slab * 64, kvh, e * bs);
+        armed = ++ring;
+      };
+      const int kt_lo = it.key_lo / kTcKeys;
+      auto below = [&](int kt) {  // the next tile down that either query tile needs
+        do --kt;
+        while (kt >= kt_lo && !rl_needs(it, 0, kt) && !rl_needs(it, 1, kt));
+        return kt;
+      };
+      int kt = below((it.key_hi + kTcKeys - 1) / kTcKeys);
+      int e = entry(kt);
+      bool first = true;
+      while (kt >= kt_lo && ok) {
+        load(kt, e, false);
+        if (first && ok) {  // Q after the first K tile, which waits for less
+          first = false;
+          if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar_qfull, 2 * Lay::kTile);
+            for (int q = 0; q < 2; ++q)
+              for (int s = 0; s < kSlabs; ++s)
+                tma_load_3d(sm + q * Lay::kTile + s * Lay::kSlab, &tmQ, bar_qfull, s * 64, it.head0,
+                            it.q_row + it.tok0 + q * tpt);
+          }
+          ++q_loads;
+        }
+        const int next = below(kt);
+        const int e_next = next >= kt_lo ? entry(next) : -1;
+        if (ok) load(kt, e, true);
+        kt = next;
+        e = e_next;
+      }
+    }
+    if (ok) {
+      RlItem stop;
+      stop.seq = -1;
+      hand_on(stop);
+    }
+    // At exit no copy or commit is in flight: the ring's last tiles have been
+    // read, or, where a wait ran out, their copies have at least landed.
+    __syncwarp();
+    if (lane == 0) {
+      bool drained = ok;
+      if (drained) drained = drain_fills(bar_empty, armed, kRing, false);
+      if (drained && q_loads > 0) drained = mbar_wait_bounded(bar_qempty, (q_loads - 1) & 1);
+      if (!drained) {
+        if (q_loads > 0) mbar_wait_bounded(bar_qfull, (q_loads - 1) & 1);
+        drain_fills(bar_full, armed, kRing, true);
+      }
+    }
+  } else if (warp == kRlMmaWarp) {
+    if (lane == 0) {
+      // ---- MMA issue
+      constexpr uint32_t idS = tc::idesc_f16(kBf16, kTcRows, kTcKeys, false);
+      constexpr uint32_t idPV = tc::idesc_f16(kBf16, kTcRows, D, true);
+      constexpr uint32_t kHi = tc::sdesc_hi(1024);
+      const uint32_t q_lo = tc::sdesc_lo(smem_u32(sm), 16);
+      const uint32_t k_lo = tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), 16);
+      const uint32_t v_lo = tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), Lay::kSlab);
+      bool ok = true;
+      int q_loads = 0;
+      int pvs[2] = {0, 0}, outs[2] = {0, 0};  // P V products so far, items with an output so far
+      for (int k = 0; ok; ++k) {
+        const int slot = k & 1;
+        if (!mbar_wait_bounded(bar_item + slot, (k >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const RlItem it = items[slot];
+        mbar_arrive(bar_free + slot);
+        if (it.seq < 0) break;
+        if (it.key_lo >= it.key_hi) continue;
+        ok = mbar_wait_bounded(bar_qfull, q_loads & 1);
+        ++q_loads;
+        const int kt_lo = it.key_lo / kTcKeys;
+        int ring = it.ring0;  // of this step's K tile; its V is the next, the previous step's V the one before
+        bool had[2] = {false, false}, begun[2] = {false, false};
+        for (int kt = (it.key_hi + kTcKeys - 1) / kTcKeys - 1; ok && kt >= kt_lo - 1; --kt) {
+          const bool need[2] = {kt >= kt_lo && rl_needs(it, 0, kt), kt >= kt_lo && rl_needs(it, 1, kt)};
+          const bool any = need[0] || need[1];
+          if (!any && !(had[0] || had[1])) continue;  // a gap between the tiles' intervals
+          const int vslot = (ring + kRing - 1) % kRing, kslot = ring % kRing;
+          bool v_seen = false, k_seen = false;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t tS = tmem + q * 128, tO = tmem + 256 + q * D;
+            if (ok && had[q]) {
+              if (!v_seen) ok = mbar_wait_bounded(bar_full + vslot, ((ring - 1) / kRing) & 1);
+              v_seen = true;
+              ok = ok && mbar_wait_bounded(bar_p + q, pvs[q] & 1);
+              // a new item's O overwrites the previous one's, which has to be read
+              if (!begun[q] && outs[q] > 0) ok = ok && mbar_wait_bounded(bar_o + q, (outs[q] - 1) & 1);
+              if (!ok) break;
+              tc::fence_after();
+              const uint32_t b_lo = v_lo + vslot * (Lay::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                tc::mma_f16_ts_words(tO, tS + 64 + kk * 8, b_lo + kk * 128, kHi, idPV, (begun[q] || kk > 0) ? 1u : 0u);
+              begun[q] = true;
+              tc::commit(bar_pv + q);
+              ++pvs[q];
+              if (q == 1 || !had[1]) tc::commit(bar_empty + vslot);
+            }
+            if (ok && need[q]) {
+              if (!k_seen) ok = mbar_wait_bounded(bar_full + kslot, (ring / kRing) & 1);
+              k_seen = true;
+              // S overwrites the tile's last P, whose product must be done
+              if (pvs[q] > 0) ok = ok && mbar_wait_bounded(bar_pv + q, (pvs[q] - 1) & 1);
+              if (!ok) break;
+              tc::fence_after();
+              const uint32_t a_lo = q_lo + q * (Lay::kTile >> 4), b_lo = k_lo + kslot * (Lay::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * Lay::kSlab + (kk & 3) * 32) >> 4;  // 64-dim slab, 16-dim step
+                if (kk == 0) tc::mma_f16_words<false>(tS, a_lo + off, kHi, b_lo + off, kHi, idS);
+                else tc::mma_f16_words<true>(tS, a_lo + off, kHi, b_lo + off, kHi, idS);
+              }
+              tc::commit(bar_s + q);
+              if (q == 1 || !need[1]) {
+                tc::commit(bar_empty + kslot);
+                if (kt == kt_lo) tc::commit(bar_qempty);  // the item's last S
+              }
+            }
+          }
+          had[0] = need[0];
+          had[1] = need[1];
+          if (any) ring += 2;
+        }
+        outs[0] += it.tile_lo[0] < it.tile_hi[0];
+        outs[1] += it.tile_lo[1] < it.tile_hi[1];
+      }
+      if (!ok) {  // a wait ran out: what was issued ends before the tensor memory goes
+        tc::commit(bar_end);
+        mbar_wait_bounded(bar_end, 0);
+      }
+    }
+  } else {
+    // ---- softmax of query tile q: thread t of the tile's warp w owns row 32 w + t
+    const int q = warp / kRlSoftWarps, wq = warp % kRlSoftWarps, r = wq * 32 + lane;
+    const uint32_t tS = tmem + q * 128 + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tO = tmem + 256 + q * D + (static_cast<uint32_t>(wq * 32) << 16);
+    const int hh = r & (hg - 1), tok = q * tpt + (r >> p.hg_log2);
+    const float c2 = p.scale_log2;
+    const uint64_t c2x2 = tc::f2(c2, c2);
+    const RlCap cap(p.rules.cap_arg, c2);
+    // the references' slack, as in the plain kernel: P stays <= 2^8, and a
+    // row's first key is at most 2^8 (fp16: not at all) below the reference
+    constexpr float kSlack = 8.f, kLow = kBf16 ? 8.f : 0.f;
+    bool ok = true;
+    int scores = 0;  // S tiles so far
+    for (int k = 0;; ++k) {
+      const int slot = k & 1;
+      // the warp goes on as one: a wait that ran out for a lane ends it for all
+      if (!__all_sync(0xffffffffu, ok && mbar_wait_bounded(bar_item + slot, (k >> 1) & 1))) break;
+      const RlItem it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free + slot);
+      if (it.seq < 0) break;
+      const int t = it.tok0 + tok;
+      const bool real = t < it.n;
+      const int pos = it.ctx + t, head = it.head0 + hh;
+      KeySpan span{0, 0};
+      if (real) span = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, pos, it.len);
+      float slope = 0.f;
+      if constexpr (BIAS) slope = __ldg(p.rules.slopes + head) * kLog2e;
+      // P, O and the sum are relative to m_ref, 0 until the row's scores call for another
+      float m_ref = 0.f, l = 0.f;
+      int ring = it.ring0;
+      bool begun = false;
+      for (int kt = (it.key_hi + kTcKeys - 1) / kTcKeys - 1; kt >= it.key_lo / kTcKeys; --kt) {
+        if (!rl_needs(it, 0, kt) && !rl_needs(it, 1, kt)) continue;
+        ring += 2;
+        if (!rl_needs(it, q, kt)) continue;
+        // after a timeout (recorded) the remaining waits are skipped
+        if (ok && !mbar_wait_bounded(bar_s + q, scores & 1)) ok = false;
+        ++scores;
+        tc::fence_after();
+        const int k0 = kt * kTcKeys;
+        // columns lo .. hi - 1 are keys of this row
+        const int lo = span.lo - k0, hi = span.hi - k0;
+        // some row of the warp does not see all of the tile, or (with a bias) sees ahead
+        const bool part = __any_sync(0xffffffffu, lo > 0 || hi < kTcKeys || (BIAS && pos - k0 < kTcKeys - 1));
+        const float ahead = static_cast<float>(pos - k0);  // distance of column 0
+        uint32_t s[64], ph[32];
+        uint64_t ls[2];
+        float me, big;
+        // One pass over the row's 128 S values, in two halves of 64 registers
+        // (keys 64-127, then 0-63): e = score - m_ref (keys the row does not
+        // see: -inf), P = exp2(e) rounded to T, two keys to a column, the
+        // tile's largest e, and with a cap the largest z^2 (above 1 the
+        // polynomial does not hold and the pass is repeated in the exact form).
+        auto pass = [&](bool exact) {
+          ls[0] = ls[1] = tc::f2(0.f, 0.f);
+          me = -INFINITY;
+          big = 0.f;
+#pragma unroll 1
+          for (int h = 1; h >= 0; --h) {
+            tc::ld_32x32b_x32(tS + 64 * h, s);
+            tc::ld_32x32b_x32(tS + 64 * h + 32, s + 32);
+            tc::wait_ld();
+            float ma = -INFINITY, mb = -INFINITY, za = 0.f;
+            if (CAP && exact) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int c = 64 * h + 2 * i;
+                float e2[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float x = soft_cap(__uint_as_float(s[2 * i + j]), c2, p.rules.cap_log2, p.rules.cap_arg);
+                  if (BIAS) x = fmaf(-slope, fabsf(ahead - (c + j)), x);
+                  e2[j] = c + j >= lo && c + j < hi ? x - m_ref : -INFINITY;
+                }
+                softmax_pair<T>(make_float2(e2[0], e2[1]), i, ma, mb, ls, s);
+              }
+            } else {
+              // e = score + base; the bias falls by slope a column towards the row's own key
+              const uint64_t negm = tc::f2(-m_ref, -m_ref);
+              const float b0 = BIAS ? fmaf(-slope, ahead - 64 * h, -m_ref) : 0.f;
+              const uint64_t sl2 = tc::f2(slope, slope), b0x2 = tc::f2(b0, b0);
+              auto score = [&](uint64_t d, uint64_t base) {
+                if constexpr (CAP) {
+                  const uint64_t z = tc::fmul2(d, cap.arg), u = tc::fmul2(z, z);
+                  const float2 u2 = tc::f2_split(u);
+                  za = max3(za, u2.x, u2.y);
+                  uint64_t y = tc::ffma2(cap.c[5], u, cap.c[4]);
+#pragma unroll
+                  for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, cap.c[j]);
+                  return tc::f2_split(tc::ffma2(d, y, base));
+                } else {
+                  return tc::f2_split(tc::ffma2(d, c2x2, base));
+                }
+              };
+              if (part) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const int c = 64 * h + 2 * i;
+                  const bool in0 = c >= lo && c < hi, in1 = c + 1 >= lo && c + 1 < hi;
+                  const uint64_t d = tc::f2(in0 ? __uint_as_float(s[2 * i]) : 0.f,
+                                            in1 ? __uint_as_float(s[2 * i + 1]) : 0.f);
+                  uint64_t base = negm;
+                  if constexpr (BIAS)
+                    base = tc::f2(fmaf(-slope, fabsf(ahead - c), -m_ref), fmaf(-slope, fabsf(ahead - (c + 1)), -m_ref));
+                  float2 e = score(d, base);
+                  e.x = in0 ? e.x : -INFINITY;
+                  e.y = in1 ? e.y : -INFINITY;
+                  softmax_pair<T>(e, i, ma, mb, ls, s);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const uint64_t d = tc::f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                  uint64_t base = negm;
+                  if constexpr (BIAS) base = tc::ffma2(sl2, tc::f2(2.f * i, 2.f * i + 1.f), b0x2);
+                  softmax_pair<T>(score(d, base), i, ma, mb, ls, s);
+                }
+              }
+            }
+            me = max3(me, ma, mb);
+            big = fmaxf(big, za);
+            if (h == 1) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ph[i] = s[i];
+            }
+          }
+        };
+        bool rescale = false, exact = false;
+        float alpha = 1.f;
+#pragma unroll 1
+        for (;;) {
+          pass(exact);
+          if (CAP && !exact && __any_sync(0xffffffffu, big > 1.f)) {
+            exact = true;  // from the top, with the reference it had
+            continue;
+          }
+          if (rescale) break;
+          // me = -inf: no key of the row in the tile
+          const bool need = me > kSlack || (l == 0.f && me != -INFINITY && me < -kLow);
+          rescale = __any_sync(0xffffffffu, need);
+          if (!rescale) break;
+          // a row that does not need it keeps its reference (alpha 1)
+          const float m_new = need ? m_ref + me : m_ref;
+          // before the row's first key of weight l and O are 0: nothing to rescale
+          alpha = l == 0.f ? 1.f : fast_exp2(m_ref - m_new);
+          l *= alpha;
+          m_ref = m_new;
+        }
+        tc::st_32x32b_x32(tS + 64, s);
+        tc::st_32x32b_x32(tS + 96, ph);
+        {
+          const float2 a = tc::f2_split(ls[0]), b = tc::f2_split(ls[1]);
+          l += (a.x + a.y) + (b.x + b.y);
+        }
+        // V rows z0 .. z1 - 1 have a weight somewhere
+        const int z0 = max(it.key_lo - k0, 0), z1 = min(it.key_hi - k0, kTcKeys);
+        if (z0 > 0 || z1 < kTcKeys) {
+          const int vr = ring - 1;  // (both tiles' warps clear the same rows, each before its own P V)
+          if (ok && !mbar_wait_bounded(bar_full + vr % kRing, (vr / kRing) & 1)) ok = false;
+          uint8_t* vt = sm + Lay::kOffRing + (vr % kRing) * Lay::kTile;
+#pragma unroll 1
+          for (int i = r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += kTcRows) {
+            const int row = i / (kSlabs * 8), rest = i % (kSlabs * 8);
+            const int at = row < z0 ? row : row - z0 + z1;
+            *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + at * 128 + (rest & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();  // the zeros are read by the tensor cores
+        }
+        if (rescale && begun) {
+          // O holds the tiles before this one: their P V were done before this S was written
+          const uint64_t a2 = tc::f2(alpha, alpha);
+#pragma unroll
+          for (int oc = 0; oc < D; oc += 32) {
+            uint32_t w[32];
+            tc::ld_32x32b_x32(tO + oc, w);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 y = tc::f2_split(tc::fmul2(tc::f2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), a2));
+              w[j] = __float_as_uint(y.x);
+              w[j + 1] = __float_as_uint(y.y);
+            }
+            tc::st_32x32b_x32(tO + oc, w);
+          }
+        }
+        begun = true;
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p + q);
+      }
+      T* orow = static_cast<T*>(p.out) + (static_cast<int64_t>(it.q_row + t) * p.num_heads + head) * D;
+      if (!begun) {  // the tile sees no key
+        if (real)
+          for (int oc = 0; oc < D; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (ok && !mbar_wait_bounded(bar_pv + q, (scores - 1) & 1)) ok = false;
+      tc::fence_after();
+      const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+#pragma unroll 1
+      for (int oc = 0; oc < D; oc += 32) {
+        uint32_t w[32];
+        tc::ld_32x32b_x32(tO + oc, w);
+        tc::wait_ld();
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          o[j] = Mma<T>::pack(__uint_as_float(w[2 * j]) * inv, __uint_as_float(w[2 * j + 1]) * inv);
+        if (ok && real) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4*>(orow + oc)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_o + q);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kRlMmaWarp) {
+    __syncwarp();
+    tc::fence_after();
+    tc::dealloc(tmem, kRlCols);
+  }
+}
+
+template <typename T, int D, bool CAP, bool BIAS>
+cudaError_t launch_rules(const RulesPrefillParams& p, int max_query_len, const CUtensorMap& mq, const CUtensorMap& mk,
+                         const CUtensorMap& mv, cudaStream_t st) {
+  constexpr int kSmem = RlLayout<D>::kSmem;
+  auto kern = prefill_rules_kernel<T, D, CAP, BIAS>;
+  static int sms[64] = {0};  // per device, set once the kernel may use its shared memory there
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!sms[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sms[dev] = n > 0 ? n : 1;
+  }
+  const int tokens = 2 * (kTcRows >> p.hg_log2);  // chunk tokens of an item
+  const int64_t pairs = (static_cast<int64_t>(max_query_len) + tokens - 1) / tokens;
+  const int64_t items = pairs * (p.num_heads >> p.hg_log2) * p.num_seqs;
+  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+  RulesPrefillParams a = p;
+  a.row_tiles = static_cast<int32_t>(pairs);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sms[dev]));
+  kern<<<grid, kRlThreads, kSmem, st>>>(a, mq, mk, mv);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_rules_form(const RulesPrefillParams& p, int max_query_len, const CUtensorMap& mq,
+                              const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  const bool cap = p.rules.cap_log2 > 0.f, bias = p.rules.slopes != nullptr;
+  if (cap) return bias ? launch_rules<T, D, true, true>(p, max_query_len, mq, mk, mv, st)
+                       : launch_rules<T, D, true, false>(p, max_query_len, mq, mk, mv, st);
+  return bias ? launch_rules<T, D, false, true>(p, max_query_len, mq, mk, mv, st)
+              : launch_rules<T, D, false, false>(p, max_query_len, mq, mk, mv, st);
+}
+
+}  // namespace
+}  // namespace pagedkv
 
 using namespace pagedkv;
 
@@ -20,8 +683,26 @@ extern "C" int paged_prefill_attention_rules(
                      scale, dtype, &p);
   if (s != KV_OK || p.num_seqs == 0) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == KV_DTYPE_F16 ? launch_prefill<__half>(p, head_dim, max_query_len, st)
-                                              : launch_prefill<__nv_bfloat16>(p, head_dim, max_query_len, st);
+  if (!tc_supported(block_size)) {
+    const cudaError_t e = dtype == KV_DTYPE_F16 ? launch_prefill<__half>(p, head_dim, max_query_len, st)
+                                                : launch_prefill<__nv_bfloat16>(p, head_dim, max_query_len, st);
+    return cuda_status(e);
+  }
+  p.test_skip = debug_skip_tile();
+  while (p.hg_log2 < 3 && p.group % (2 << p.hg_log2) == 0) ++p.hg_log2;
+  CUtensorMap mq, mk, mv;
+  const int64_t rows = num_blocks * block_size;
+  if (!tc_map(q, head_dim, num_heads, num_query_tokens, 1 << p.hg_log2, kTcRows >> p.hg_log2, &mq) ||
+      !tc_map(k_cache, head_dim, num_kv_heads, rows, 1, block_size, &mk) ||
+      !tc_map(v_cache, head_dim, num_kv_heads, rows, 1, block_size, &mv))
+    return cuda_status(cudaErrorInvalidValue, "cuTensorMapEncodeTiled failed");
+  cudaError_t e;
+  if (dtype == KV_DTYPE_F16)
+    e = head_dim == 64 ? launch_rules_form<__half, 64>(p, max_query_len, mq, mk, mv, st)
+                       : launch_rules_form<__half, 128>(p, max_query_len, mq, mk, mv, st);
+  else
+    e = head_dim == 64 ? launch_rules_form<__nv_bfloat16, 64>(p, max_query_len, mq, mk, mv, st)
+                       : launch_rules_form<__nv_bfloat16, 128>(p, max_query_len, mq, mk, mv, st);
   return cuda_status(e);
 }
 

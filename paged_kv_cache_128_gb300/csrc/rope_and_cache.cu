@@ -84,8 +84,13 @@ struct RopeParams {
   uint64_t axis_of_pair[kRopeAxisPairs / 32];
 };
 
-__device__ __forceinline__ int rope_axis(const RopeParams& p, int pair) {
-  return static_cast<int>(p.axis_of_pair[pair >> 5] >> (2 * (pair & 31))) & 3;
+// The position that pair `pair` of a token turns by.
+__device__ __forceinline__ int32_t rope_position(const RopeParams& p, const int32_t (&pos)[kRopeAxes], int pair) {
+  const int axis = static_cast<int>(p.axis_of_pair[pair >> 5] >> (2 * (pair & 31))) & 3;
+  int32_t at = pos[0];
+#pragma unroll
+  for (int a = 1; a < kRopeAxes; ++a) at = axis == a ? pos[a] : at;
+  return at;
 }
 
 // Position and slot of token t; false when the token is padded or out of
@@ -199,27 +204,37 @@ rope_cache_kernel(const RopeParams p, int threads) {
   load(first);
   const bool reporter = tid == 0 && blockIdx.y == 0;
   if (AXES ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) return;
+  // With several axes the CTA first gathers the token's own row of angles, a
+  // thread per pair from its axis' row of the table (each lane picking its
+  // pairs from up to four rows took 40 registers into spills: 43.0 us instead
+  // of 32.8 for 8192 tokens of 28 + 2 x 4 heads of 128).
+  const float* row;
+  __shared__ __align__(16) float own_row[AXES ? 2 * kRopeAxisPairs : 4];
+  if constexpr (AXES) {
+    for (int i = tid; i < half; i += threads) {
+      const float* from = p.cos_sin + rope_position(p, pos, i) * static_cast<int64_t>(p.rot_dim) + i;
+      own_row[i] = __ldg(from);
+      own_row[half + i] = __ldg(from + half);
+    }
+    __syncthreads();
+    row = own_row + col * 8;
+  } else {
+    row = p.cos_sin + static_cast<int64_t>(pos[0]) * p.rot_dim + col * 8;
+  }
   float c[8], s[8];
   if (turn) {
-    // the lane's eight pairs; with several axes each axis' row gives those of
-    // them that are its own (an axis none of them has is not read)
-    const uint32_t mine = AXES ? static_cast<uint32_t>(p.axis_of_pair[col >> 2] >> (16 * (col & 3))) & 0xffffu : 0u;
 #pragma unroll
-    for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a) {
-      uint32_t own[8], any = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) any |= own[i] = !AXES || ((mine >> (2 * i)) & 3u) == static_cast<uint32_t>(a);
-      if (AXES && !any) continue;
-      const float* row = p.cos_sin + static_cast<int64_t>(pos[a]) * p.rot_dim + col * 8;
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i));
-        if (own[i]) c[i] = cv.x, s[i] = sv.x;
-        if (own[i + 1]) c[i + 1] = cv.y, s[i + 1] = sv.y;
-        if (own[i + 2]) c[i + 2] = cv.z, s[i + 2] = sv.z;
-        if (own[i + 3]) c[i + 3] = cv.w, s[i + 3] = sv.w;
+    for (int i = 0; i < 8; i += 4) {
+      float4 cv, sv;
+      if constexpr (AXES) {
+        cv = *reinterpret_cast<const float4*>(row + i);
+        sv = *reinterpret_cast<const float4*>(row + half + i);
+      } else {
+        cv = __ldg(reinterpret_cast<const float4*>(row + i));
+        sv = __ldg(reinterpret_cast<const float4*>(row + half + i));
       }
+      c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
+      s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
     }
   }
   const int64_t blk = slot / p.block_size, off = slot % p.block_size;
@@ -314,13 +329,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_any_kernel(const Rope
                         : static_cast<const T*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) +
                               static_cast<int64_t>(hk) * D;
     auto row_of = [&](int i) {  // the table row of pair i
-      int32_t at = pos[0];
-      if constexpr (AXES) {
-        const int axis = rope_axis(p, i);
-#pragma unroll
-        for (int a = 1; a < kRopeAxes; ++a) at = axis == a ? pos[a] : at;
-      }
-      return p.cos_sin + static_cast<int64_t>(at) * p.rot_dim;
+      return p.cos_sin + static_cast<int64_t>(AXES ? rope_position(p, pos, i) : pos[0]) * p.rot_dim;
     };
     const int turned = is_v ? 0 : p.rot_dim;
     // visit(e, y): every output value of the row once, pairs first
