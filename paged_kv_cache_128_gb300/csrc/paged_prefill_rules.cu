@@ -40,19 +40,20 @@ namespace {
 //     per thread, as in the plain kernel.
 // V rows that lie in no row's interval are cleared before P V reads them.
 // ---------------------------------------------------------------------------
-constexpr int kRlSoftWarps = 4;  // per query tile
+constexpr int kRlSoftWarps = 8;  // per query tile: a row's keys are halved between two warps
 constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1;
 constexpr int kRlThreads = 32 * (kRlTmaWarp + 1);
 constexpr uint32_t kRlCols = 512;
 
 template <int D>
 struct RlLayout {
-  static constexpr int kRing = D == 64 ? 8 : 5;      // K and V tile slots
+  static constexpr int kRing = D == 64 ? 8 : 4;      // K and V tile slots
   static constexpr int kSlab = kTcRows * 128;        // one 64-column slab of 128 rows
   static constexpr int kTile = (D / 64) * kSlab;     // a Q, K or V tile
   static constexpr int kOffRing = 2 * kTile;         // after the two Q tiles
   static constexpr int kOffBar = kOffRing + kRing * kTile;
-  static constexpr int kBytes = kOffBar + 512;
+  static constexpr int kOffRow = kOffBar + 512;       // [query tile][half][row] floats: a half's maxima and sums
+  static constexpr int kBytes = kOffRow + 2 * 2 * kTcRows * 4;
   static constexpr int kSmem = kBytes + 1024;        // slack for 1024-byte alignment
 };
 
@@ -84,6 +85,33 @@ struct RlCap {
     for (int i = 0; i < 6; ++i) c[i] = tc::f2(k[i] * scale_log2, k[i] * scale_log2);
   }
 };
+
+// sum += both halves of a packed pair, in float32.
+template <typename T>
+__device__ __forceinline__ void add_pair(float& sum, uint32_t w) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %0, h, %0;\n\t}"
+        : "+f"(sum)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %0, h, %0;\n\t}"
+        : "+f"(sum)
+        : "r"(w));
+}
+
+// Barrier `id` over `threads` threads, with the OR of their predicates.
+__device__ __forceinline__ bool barrier_or(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
 
 template <typename T, int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kRlThreads, 1)
@@ -394,23 +422,26 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       }
     }
   } else {
-    // ---- softmax of query tile q: thread t of the tile's warp w owns row 32 w + t
-    const int q = warp / kRlSoftWarps, wq = warp % kRlSoftWarps, r = wq * 32 + lane;
+    // ---- softmax of query tile q: thread t of the tile's warps w and w + 4 has
+    // row 32 w + t, the first its keys 0-63 and the second its keys 64-127
+    const int q = warp / kRlSoftWarps, wq = warp & 3, half = (warp >> 2) & 1, r = wq * 32 + lane;
     const uint32_t tS = tmem + q * 128 + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tO = tmem + 256 + q * D + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tO = tmem + 256 + q * D + half * (D / 2) + (static_cast<uint32_t>(wq * 32) << 16);
     const int hh = r & (hg - 1), tok = q * tpt + (r >> p.hg_log2);
+    const int pair = 1 + q * 4 + wq;  // named barrier of the two warps of a row
+    float* const row_own = reinterpret_cast<float*>(sm + Lay::kOffRow) + (q * 2 + half) * kTcRows + r;
+    const float* const row_other = row_own + (half ? -kTcRows : kTcRows);
     const float c2 = p.scale_log2;
     const uint64_t c2x2 = tc::f2(c2, c2);
     const RlCap cap(p.rules.cap_arg, c2);
-    // the references' slack, as in the plain kernel: P stays <= 2^8, and a
-    // row's first key is at most 2^8 (fp16: not at all) below the reference
-    constexpr float kSlack = 8.f, kLow = kBf16 ? 8.f : 0.f;
+    // a tile whose weights sum to more than this has moved too far above its row's reference
+    constexpr float kGrown = kBf16 ? 1.0995116e12f : 16384.f;  // 2^40: fp32 sums; 2^14: fp16 weights
     bool ok = true;
     int scores = 0;  // S tiles so far
     for (int k = 0;; ++k) {
       const int slot = k & 1;
-      // the warp goes on as one: a wait that ran out for a lane ends it for all
-      if (!__all_sync(0xffffffffu, ok && mbar_wait_bounded(bar_item + slot, (k >> 1) & 1))) break;
+      // a row's two warps go on together: a wait that ran out for a lane of either ends both
+      if (barrier_or(pair, 64, !(ok && mbar_wait_bounded(bar_item + slot, (k >> 1) & 1)))) break;
       const RlItem it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_free + slot);
@@ -422,10 +453,12 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       if (real) span = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, pos, it.len);
       float slope = 0.f;
       if constexpr (BIAS) slope = __ldg(p.rules.slopes + head) * kLog2e;
-      // P, O and the sum are relative to m_ref, 0 until the row's scores call for another
+      // Weights and sums are relative to m_ref, the largest score of the first
+      // tile in which the row sees a key (set: there was one).  It moves again
+      // only when a tile's weights sum to more than kGrown.
       float m_ref = 0.f, l = 0.f;
+      bool set = false, begun = false;
       int ring = it.ring0;
-      bool begun = false;
       for (int kt = (it.key_hi + kTcKeys - 1) / kTcKeys - 1; kt >= it.key_lo / kTcKeys; --kt) {
         if (!rl_needs(it, 0, kt) && !rl_needs(it, 1, kt)) continue;
         ring += 2;
@@ -434,129 +467,152 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         if (ok && !mbar_wait_bounded(bar_s + q, scores & 1)) ok = false;
         ++scores;
         tc::fence_after();
-        const int k0 = kt * kTcKeys;
+        const int k0 = kt * kTcKeys + 64 * half;  // this half's first key
         // columns lo .. hi - 1 are keys of this row
         const int lo = span.lo - k0, hi = span.hi - k0;
-        // some row of the warp does not see all of the tile, or (with a bias) sees ahead
-        const bool part = __any_sync(0xffffffffu, lo > 0 || hi < kTcKeys || (BIAS && pos - k0 < kTcKeys - 1));
+        // some row of the warp does not see all of the half, or (with a bias) sees ahead
+        const bool part = __any_sync(0xffffffffu, lo > 0 || hi < 64 || (BIAS && pos - k0 < 63));
         const float ahead = static_cast<float>(pos - k0);  // distance of column 0
-        uint32_t s[64], ph[32];
-        uint64_t ls[2];
-        float me, big;
-        // One pass over the row's 128 S values, in two halves of 64 registers
-        // (keys 64-127, then 0-63): e = score - m_ref (keys the row does not
-        // see: -inf), P = exp2(e) rounded to T, two keys to a column, the
-        // tile's largest e, and with a cap the largest z^2 (above 1 the
-        // polynomial does not hold and the pass is repeated in the exact form).
-        auto pass = [&](bool exact) {
-          ls[0] = ls[1] = tc::f2(0.f, 0.f);
-          me = -INFINITY;
-          big = 0.f;
+        const uint32_t tSh = tS + 64 * half;
+        uint32_t pk[32];  // P, two keys to a column
+        float sum;
+        // The half's largest score, over the row with the other warp's.
+        auto row_max = [&]() {
+          float m = -INFINITY;
 #pragma unroll 1
-          for (int h = 1; h >= 0; --h) {
-            tc::ld_32x32b_x32(tS + 64 * h, s);
-            tc::ld_32x32b_x32(tS + 64 * h + 32, s + 32);
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            uint32_t s[32];
+            tc::ld_32x32b_x32(tSh + c0, s);
             tc::wait_ld();
-            float ma = -INFINITY, mb = -INFINITY, za = 0.f;
-            if (CAP && exact) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int c = 64 * h + 2 * i;
-                float e2[2];
+            for (int i = 0; i < 32; ++i) {
+              const int c = c0 + i;
+              float x = __uint_as_float(s[i]);
+              x = CAP ? soft_cap(x, c2, p.rules.cap_log2, p.rules.cap_arg) : x * c2;
+              if (BIAS) x = fmaf(-slope, fabsf(ahead - c), x);
+              if (c >= lo && c < hi) m = fmaxf(m, x);
+            }
+          }
+          *row_own = m;
+          named_barrier_sync(pair, 64);
+          m = fmaxf(m, *row_other);
+          named_barrier_sync(pair, 64);  // read before it is written again
+          return m;
+        };
+        // P = exp2(score - m_ref) rounded to T (keys the row does not see: 0), and
+        // the sum of the rounded P.  `masked`: some key is not seen.  `in_full`: the
+        // cap in its exact form, for scores beyond it, where the polynomial does
+        // not hold (true returned: it was needed and not used).
+        auto pass = [&](auto masked, auto in_full) -> bool {
+          constexpr bool kPart = decltype(masked)::value, kExact = decltype(in_full)::value;
+          float s0 = 0.f, s1 = 0.f, big = 0.f;
+          const uint64_t negm = tc::f2(-m_ref, -m_ref);
+          const uint64_t sl2 = tc::f2(slope, slope);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float x = soft_cap(__uint_as_float(s[2 * i + j]), c2, p.rules.cap_log2, p.rules.cap_arg);
-                  if (BIAS) x = fmaf(-slope, fabsf(ahead - (c + j)), x);
-                  e2[j] = c + j >= lo && c + j < hi ? x - m_ref : -INFINITY;
-                }
-                softmax_pair<T>(make_float2(e2[0], e2[1]), i, ma, mb, ls, s);
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            uint32_t s[32];
+            tc::ld_32x32b_x32(tSh + c0, s);
+            tc::wait_ld();
+            const float b0 = BIAS ? fmaf(-slope, ahead - c0, -m_ref) : 0.f;
+            const uint64_t b0x2 = tc::f2(b0, b0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int c = c0 + 2 * i;
+              float2 x = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), e;
+              const bool in0 = !kPart || (c >= lo && c < hi), in1 = !kPart || (c + 1 >= lo && c + 1 < hi);
+              uint64_t base = negm;
+              if constexpr (BIAS) {
+                if (kPart) base = tc::f2(fmaf(-slope, fabsf(ahead - c), -m_ref), fmaf(-slope, fabsf(ahead - (c + 1)), -m_ref));
+                else base = tc::ffma2(sl2, tc::f2(2.f * i, 2.f * i + 1.f), b0x2);
               }
-            } else {
-              // e = score + base; the bias falls by slope a column towards the row's own key
-              const uint64_t negm = tc::f2(-m_ref, -m_ref);
-              const float b0 = BIAS ? fmaf(-slope, ahead - 64 * h, -m_ref) : 0.f;
-              const uint64_t sl2 = tc::f2(slope, slope), b0x2 = tc::f2(b0, b0);
-              auto score = [&](uint64_t d, uint64_t base) {
-                if constexpr (CAP) {
-                  const uint64_t z = tc::fmul2(d, cap.arg), u = tc::fmul2(z, z);
-                  const float2 u2 = tc::f2_split(u);
-                  za = max3(za, u2.x, u2.y);
-                  uint64_t y = tc::ffma2(cap.c[5], u, cap.c[4]);
-#pragma unroll
-                  for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, cap.c[j]);
-                  return tc::f2_split(tc::ffma2(d, y, base));
-                } else {
-                  return tc::f2_split(tc::ffma2(d, c2x2, base));
+              if constexpr (CAP && kExact) {
+                const float2 b = tc::f2_split(base);
+                e.x = soft_cap(x.x, c2, p.rules.cap_log2, p.rules.cap_arg) + b.x;
+                e.y = soft_cap(x.y, c2, p.rules.cap_log2, p.rules.cap_arg) + b.y;
+              } else if constexpr (CAP) {
+                if (kPart) {  // what lies in a slot that is not seen must not call for the exact form
+                  x.x = in0 ? x.x : 0.f;
+                  x.y = in1 ? x.y : 0.f;
                 }
-              };
-              if (part) {
+                const uint64_t d = tc::f2(x.x, x.y), z = tc::fmul2(d, cap.arg), u = tc::fmul2(z, z);
+                const float2 u2 = tc::f2_split(u);
+                big = max3(big, u2.x, u2.y);
+                uint64_t y = tc::ffma2(cap.c[5], u, cap.c[4]);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const int c = 64 * h + 2 * i;
-                  const bool in0 = c >= lo && c < hi, in1 = c + 1 >= lo && c + 1 < hi;
-                  const uint64_t d = tc::f2(in0 ? __uint_as_float(s[2 * i]) : 0.f,
-                                            in1 ? __uint_as_float(s[2 * i + 1]) : 0.f);
-                  uint64_t base = negm;
-                  if constexpr (BIAS)
-                    base = tc::f2(fmaf(-slope, fabsf(ahead - c), -m_ref), fmaf(-slope, fabsf(ahead - (c + 1)), -m_ref));
-                  float2 e = score(d, base);
-                  e.x = in0 ? e.x : -INFINITY;
-                  e.y = in1 ? e.y : -INFINITY;
-                  softmax_pair<T>(e, i, ma, mb, ls, s);
-                }
+                for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, cap.c[j]);
+                e = tc::f2_split(tc::ffma2(d, y, base));
               } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const uint64_t d = tc::f2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                  uint64_t base = negm;
-                  if constexpr (BIAS) base = tc::ffma2(sl2, tc::f2(2.f * i, 2.f * i + 1.f), b0x2);
-                  softmax_pair<T>(score(d, base), i, ma, mb, ls, s);
-                }
+                e = tc::f2_split(tc::ffma2(tc::f2(x.x, x.y), c2x2, base));
               }
+              if (kPart) {
+                e.x = in0 ? e.x : -INFINITY;
+                e.y = in1 ? e.y : -INFINITY;
+              }
+              const uint32_t w = Mma<T>::pack(fast_exp2(e.x), fast_exp2(e.y));
+              pk[c / 2] = w;
+              // the sum is taken over the rounded P that P V multiplies, so that the
+              // weights the output is normalised by are the ones it was built from
+              if (i & 1) add_pair<T>(s1, w);
+              else add_pair<T>(s0, w);
             }
-            me = max3(me, ma, mb);
-            big = fmaxf(big, za);
-            if (h == 1) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) ph[i] = s[i];
-            }
+          }
+          sum = s0 + s1;
+          return CAP && !kExact && __any_sync(0xffffffffu, big > 1.f);
+        };
+        auto weigh = [&]() {
+          using std::false_type;
+          using std::true_type;
+          const bool beyond = part ? pass(true_type(), false_type()) : pass(false_type(), false_type());
+          if constexpr (CAP) {
+            if (beyond) pass(true_type(), true_type());
           }
         };
-        bool rescale = false, exact = false;
-        float alpha = 1.f;
-#pragma unroll 1
-        for (;;) {
-          pass(exact);
-          if (CAP && !exact && __any_sync(0xffffffffu, big > 1.f)) {
-            exact = true;  // from the top, with the reference it had
-            continue;
+        // (both warps of a row know the same `set`, so they agree on what follows)
+        if (!__all_sync(0xffffffffu, set)) {
+          const float m = row_max();
+          if (!set && m != -INFINITY) {
+            m_ref = m;
+            set = true;
           }
-          if (rescale) break;
-          // me = -inf: no key of the row in the tile
-          const bool need = me > kSlack || (l == 0.f && me != -INFINITY && me < -kLow);
-          rescale = __any_sync(0xffffffffu, need);
-          if (!rescale) break;
-          // a row that does not need it keeps its reference (alpha 1)
-          const float m_new = need ? m_ref + me : m_ref;
-          // before the row's first key of weight l and O are 0: nothing to rescale
-          alpha = l == 0.f ? 1.f : fast_exp2(m_ref - m_new);
+        }
+        weigh();
+        // Do the row's two warps agree that the reference holds?  The barrier
+        // also says that both have read S, which P goes over.
+        if (barrier_or(pair, 64, sum > kGrown)) {
+          const float m = row_max();
+          const float m_new = fmaxf(m_ref, m), alpha = fast_exp2(m_ref - m_new);
           l *= alpha;
           m_ref = m_new;
+          if (begun) {
+            // O holds the tiles before this one: their P V were done before this S was written
+            const uint64_t a2 = tc::f2(alpha, alpha);
+#pragma unroll 1
+            for (int oc = 0; oc < D / 2; oc += 32) {
+              uint32_t w[32];
+              tc::ld_32x32b_x32(tO + oc, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 y = tc::f2_split(tc::fmul2(tc::f2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), a2));
+                w[j] = __float_as_uint(y.x);
+                w[j + 1] = __float_as_uint(y.y);
+              }
+              tc::st_32x32b_x32(tO + oc, w);
+            }
+          }
+          weigh();
+          named_barrier_sync(pair, 64);
         }
-        tc::st_32x32b_x32(tS + 64, s);
-        tc::st_32x32b_x32(tS + 96, ph);
-        {
-          const float2 a = tc::f2_split(ls[0]), b = tc::f2_split(ls[1]);
-          l += (a.x + a.y) + (b.x + b.y);
-        }
+        tc::st_32x32b_x32(tS + 64 + 32 * half, pk);
+        l += sum;
         // V rows z0 .. z1 - 1 have a weight somewhere
-        const int z0 = max(it.key_lo - k0, 0), z1 = min(it.key_hi - k0, kTcKeys);
+        const int z0 = max(it.key_lo - kt * kTcKeys, 0), z1 = min(it.key_hi - kt * kTcKeys, kTcKeys);
         if (z0 > 0 || z1 < kTcKeys) {
           const int vr = ring - 1;  // (both tiles' warps clear the same rows, each before its own P V)
           if (ok && !mbar_wait_bounded(bar_full + vr % kRing, (vr / kRing) & 1)) ok = false;
           uint8_t* vt = sm + Lay::kOffRing + (vr % kRing) * Lay::kTile;
 #pragma unroll 1
-          for (int i = r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += kTcRows) {
+          for (int i = half * kTcRows + r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += 2 * kTcRows) {
             const int row = i / (kSlabs * 8), rest = i % (kSlabs * 8);
             const int at = row < z0 ? row : row - z0 + z1;
             *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + at * 128 + (rest & 7) * 16) =
@@ -564,40 +620,27 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           }
           fence_proxy_async_smem();  // the zeros are read by the tensor cores
         }
-        if (rescale && begun) {
-          // O holds the tiles before this one: their P V were done before this S was written
-          const uint64_t a2 = tc::f2(alpha, alpha);
-#pragma unroll
-          for (int oc = 0; oc < D; oc += 32) {
-            uint32_t w[32];
-            tc::ld_32x32b_x32(tO + oc, w);
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 y = tc::f2_split(tc::fmul2(tc::f2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), a2));
-              w[j] = __float_as_uint(y.x);
-              w[j + 1] = __float_as_uint(y.y);
-            }
-            tc::st_32x32b_x32(tO + oc, w);
-          }
-        }
         begun = true;
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + q);
       }
-      T* orow = static_cast<T*>(p.out) + (static_cast<int64_t>(it.q_row + t) * p.num_heads + head) * D;
+      T* orow = static_cast<T*>(p.out) + (static_cast<int64_t>(it.q_row + t) * p.num_heads + head) * D + half * (D / 2);
       if (!begun) {  // the tile sees no key
         if (real)
-          for (int oc = 0; oc < D; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
+          for (int oc = 0; oc < D / 2; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
         continue;
       }
+      *row_own = l;
+      named_barrier_sync(pair, 64);
+      l += *row_other;
+      named_barrier_sync(pair, 64);
       if (ok && !mbar_wait_bounded(bar_pv + q, (scores - 1) & 1)) ok = false;
       tc::fence_after();
       const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
 #pragma unroll 1
-      for (int oc = 0; oc < D; oc += 32) {
+      for (int oc = 0; oc < D / 2; oc += 32) {
         uint32_t w[32];
         tc::ld_32x32b_x32(tO + oc, w);
         tc::wait_ld();
