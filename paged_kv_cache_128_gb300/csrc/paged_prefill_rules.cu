@@ -30,20 +30,29 @@ namespace {
 //
 // Tensor memory (512 columns): S of the two tiles at 0 and 128 (P, two keys to
 // a column, over the upper half of its S), O at 256 and 256 + D.
-//   warp 9, scheduler and TMA producer: works out an item's ranges, hands them
+//   warp 17, scheduler and TMA producer: works out an item's ranges, hands them
 //     to the others through a two-deep ring in shared memory, and loads Q and
 //     the K and V tiles (one box per block and 64-dim slab, a lane each) into a
 //     ring of tile slots, running ahead into the next item;
-//   warp 8: one lane issues, for each key tile and for the two query tiles in
-//     turn, O += P V of the previous key tile and S = Q K^T of this one;
-//   warps 0-3 and 4-7: the softmax of the first and second query tile, a row
-//     per thread, as in the plain kernel.
+//   warp 16 issues, for each key tile and for the two query tiles in turn, O +=
+//     P V of the previous key tile and S = Q K^T of this one (a warp for each
+//     query tile was slower, 558 us for 500: their MMAs interleave, both softmaxes
+//     run at once and the tensor cores wait for both);
+//   warps 0-7 and 8-15: the softmax of the first and second query tile, half a
+//     row's keys per thread.
 // V rows that lie in no row's interval are cleared before P V reads them.
 // ---------------------------------------------------------------------------
 constexpr int kRlSoftWarps = 8;  // per query tile: a row's keys are halved between two warps
 constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1;
 constexpr int kRlThreads = 32 * (kRlTmaWarp + 1);
 constexpr uint32_t kRlCols = 512;
+
+// mbar_wait_bounded with the wait itself out of line: the many waits of this
+// kernel's roles are short in its code then, and their instructions stay cached.
+__device__ __noinline__ bool rl_wait_on(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+__device__ __forceinline__ bool rl_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || rl_wait_on(bar, parity);
+}
 
 template <int D>
 struct RlLayout {
@@ -68,21 +77,39 @@ struct RlItem {
   int ring0;                   // ring position of the item's first K tile
 };
 
-__device__ __forceinline__ bool rl_needs(const RlItem& it, int q, int kt) {
-  return kt >= it.tile_lo[q] && kt < it.tile_hi[q];
-}
+// The key tiles of an item as they are walked: first down to end, of which
+// own() says whether query tile q needs one, other() whether the other one does.
+struct RlSpan {
+  int first, end, own_lo, own_hi, other_lo, other_hi, ring0;
+  __device__ __forceinline__ RlSpan(const RlItem& it, int q)
+      : first((it.key_hi + kTcKeys - 1) / kTcKeys - 1), end(it.key_lo / kTcKeys), own_lo(it.tile_lo[q]),
+        own_hi(it.tile_hi[q]), other_lo(it.tile_lo[q ^ 1]), other_hi(it.tile_hi[q ^ 1]), ring0(it.ring0) {}
+  __device__ __forceinline__ bool own(int kt) const { return kt >= own_lo && kt < own_hi; }
+  __device__ __forceinline__ bool other(int kt) const { return kt >= other_lo && kt < other_hi; }
+  __device__ __forceinline__ bool any(int kt) const { return own(kt) || other(kt); }
+};
 
-// The polynomial of the cap for packed pairs: tanh(z) = z P(z^2) for |z| <= 1,
-// P of degree 5, within 6e-7 of it (the fit of soft_cap's, two terms shorter:
-// rounding the weights to 16 bits leaves 5e-4 and more).
+// The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
+// P(z^2) for |z| <= 1, P of degree 5, within 6e-7 of it (the fit of soft_cap's,
+// two terms shorter: rounding the weights to 16 bits leaves 5e-4 and more).
+// With z = a dot the coefficients take the powers of a^2 and scale_log2; the
+// squares of dots it holds for end at 1 / a^2.  Where a^2 is so small that
+// a^10 would leave float32 (a cap over 3000 times the scale, which no score
+// comes near to), nothing is in range and the exact form serves.
 struct RlCap {
-  uint64_t arg, c[6];  // cap_arg and the coefficients times scale_log2
+  uint64_t c[6];
+  float limit;
   __device__ __forceinline__ RlCap(float cap_arg, float scale_log2) {
     constexpr float k[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
                             -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
-    arg = tc::f2(cap_arg, cap_arg);
+    const float a2 = cap_arg * cap_arg;
+    float power = scale_log2;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) c[i] = tc::f2(k[i] * scale_log2, k[i] * scale_log2);
+    for (int i = 0; i < 6; ++i) {
+      c[i] = tc::f2(k[i] * power, k[i] * power);
+      power *= a2;
+    }
+    limit = a2 >= 1e-7f ? 1.f / a2 : -1.f;
   }
 };
 
@@ -97,6 +124,13 @@ __device__ __forceinline__ void add_pair(float& sum, uint32_t w) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %0, h, %0;\n\t}"
         : "+f"(sum)
         : "r"(w));
+}
+
+// One lane of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // Barrier `id` over `threads` threads, with the OR of their predicates.
@@ -131,7 +165,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   uint64_t* bar_pv = bar_p + 2;                 // [2] P V done
   uint64_t* bar_o = bar_pv + 2;                 // [2] O read (one arrival per softmax warp)
   uint64_t* bar_item = bar_o + 2;               // [2] item slot filled
-  uint64_t* bar_free = bar_item + 2;            // [2] item slot read (MMA lane and every softmax warp)
+  uint64_t* bar_free = bar_item + 2;            // [2] item slot read (MMA warp and every softmax warp)
   uint64_t* bar_end = bar_free + 2;             // after a wait ran out: all MMAs done
   RlItem* items = reinterpret_cast<RlItem*>(bar_end + 1);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
@@ -177,7 +211,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     // a wait by lane 0 for the whole warp
     auto wait = [&](uint64_t* bar, int parity) {
       int w = 1;
-      if (lane == 0) w = mbar_wait_bounded(bar, parity);
+      if (lane == 0) w = rl_wait(bar, parity);
       ok = __shfl_sync(0xffffffffu, w, 0) != 0;
       return ok;
     };
@@ -288,13 +322,14 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                       is_v ? &tmV : &tmK, bar_full + slot, my_slab * 64, kvh, e * bs);
         armed = ++ring;
       };
-      const int kt_lo = it.key_lo / kTcKeys;
+      const RlSpan walk(it, 0);
+      const int kt_lo = walk.end;
       auto below = [&](int kt) {  // the next tile down that either query tile needs
         do --kt;
-        while (kt >= kt_lo && !rl_needs(it, 0, kt) && !rl_needs(it, 1, kt));
+        while (kt >= kt_lo && !walk.any(kt));
         return kt;
       };
-      int kt = below((it.key_hi + kTcKeys - 1) / kTcKeys);
+      int kt = below(walk.first + 1);
       int e = entry(kt);
       bool first = true;
       while (kt >= kt_lo && ok) {
@@ -329,73 +364,80 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     if (lane == 0) {
       bool drained = ok;
       if (drained) drained = drain_fills(bar_empty, armed, kRing, false);
-      if (drained && q_loads > 0) drained = mbar_wait_bounded(bar_qempty, (q_loads - 1) & 1);
+      if (drained && q_loads > 0) drained = rl_wait(bar_qempty, (q_loads - 1) & 1);
       if (!drained) {
-        if (q_loads > 0) mbar_wait_bounded(bar_qfull, (q_loads - 1) & 1);
+        if (q_loads > 0) rl_wait(bar_qfull, (q_loads - 1) & 1);
         drain_fills(bar_full, armed, kRing, true);
       }
     }
   } else if (warp == kRlMmaWarp) {
-    if (lane == 0) {
-      // ---- MMA issue
-      constexpr uint32_t idS = tc::idesc_f16(kBf16, kTcRows, kTcKeys, false);
-      constexpr uint32_t idPV = tc::idesc_f16(kBf16, kTcRows, D, true);
-      constexpr uint32_t kHi = tc::sdesc_hi(1024);
-      const uint32_t q_lo = tc::sdesc_lo(smem_u32(sm), 16);
-      const uint32_t k_lo = tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), 16);
-      const uint32_t v_lo = tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), Lay::kSlab);
-      bool ok = true;
-      int q_loads = 0;
-      int pvs[2] = {0, 0}, outs[2] = {0, 0};  // P V products so far, items with an output so far
-      for (int k = 0; ok; ++k) {
-        const int slot = k & 1;
-        if (!mbar_wait_bounded(bar_item + slot, (k >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        const RlItem it = items[slot];
-        mbar_arrive(bar_free + slot);
-        if (it.seq < 0) break;
-        if (it.key_lo >= it.key_hi) continue;
-        ok = mbar_wait_bounded(bar_qfull, q_loads & 1);
-        ++q_loads;
-        const int kt_lo = it.key_lo / kTcKeys;
-        int ring = it.ring0;  // of this step's K tile; its V is the next, the previous step's V the one before
-        bool had[2] = {false, false}, begun[2] = {false, false};
-        for (int kt = (it.key_hi + kTcKeys - 1) / kTcKeys - 1; ok && kt >= kt_lo - 1; --kt) {
-          const bool need[2] = {kt >= kt_lo && rl_needs(it, 0, kt), kt >= kt_lo && rl_needs(it, 1, kt)};
-          const bool any = need[0] || need[1];
-          if (!any && !(had[0] || had[1])) continue;  // a gap between the tiles' intervals
-          const int vslot = (ring + kRing - 1) % kRing, kslot = ring % kRing;
-          bool v_seen = false, k_seen = false;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t tS = tmem + q * 128, tO = tmem + 256 + q * D;
-            if (ok && had[q]) {
-              if (!v_seen) ok = mbar_wait_bounded(bar_full + vslot, ((ring - 1) / kRing) & 1);
-              v_seen = true;
-              ok = ok && mbar_wait_bounded(bar_p + q, pvs[q] & 1);
-              // a new item's O overwrites the previous one's, which has to be read
-              if (!begun[q] && outs[q] > 0) ok = ok && mbar_wait_bounded(bar_o + q, (outs[q] - 1) & 1);
-              if (!ok) break;
-              tc::fence_after();
-              const uint32_t b_lo = v_lo + vslot * (Lay::kTile >> 4);
+    // ---- MMA issue.  The warp runs as one, on values that are the same in all
+    // lanes by construction (broadcasts and votes), so that the descriptors stay
+    // in uniform registers, which the MMA instructions take; one elected lane
+    // issues.  With all of it in a single lane's branch the issue of a step's
+    // products took as long as the products.
+    constexpr uint32_t idS = tc::idesc_f16(kBf16, kTcRows, kTcKeys, false);
+    constexpr uint32_t idPV = tc::idesc_f16(kBf16, kTcRows, D, true);
+    constexpr uint32_t kHi = tc::sdesc_hi(1024);
+    const bool leader = elect_one();
+    auto all = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = all(tmem);
+    const uint32_t q_lo = all(tc::sdesc_lo(smem_u32(sm), 16));
+    const uint32_t k_lo = all(tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), 16));
+    const uint32_t v_lo = all(tc::sdesc_lo(smem_u32(sm + Lay::kOffRing), Lay::kSlab));
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, rl_wait(bar, parity));
+      return ok;
+    };
+    int q_loads = 0, pvs0 = 0, pvs1 = 0;  // Q loads, P V products
+    int outs0 = 0, outs1 = 0;             // items with an output
+    int ring = 0;  // of this step's K tile; its V is the next, the previous step's V the one before
+    for (int k = 0; ok; ++k) {
+      const int slot = k & 1;
+      if (!wait(bar_item + slot, (k >> 1) & 1)) break;
+      const RlSpan mine(items[slot], 0);
+      const int last = all(items[slot].seq < 0);
+      const int first = all(mine.first), end = all(mine.end), lo0 = all(mine.own_lo), hi0 = all(mine.own_hi),
+                lo1 = all(mine.other_lo), hi1 = all(mine.other_hi);
+      __syncwarp();
+      if (leader) mbar_arrive(bar_free + slot);
+      if (last) break;
+      if (first < end) continue;
+      if (!wait(bar_qfull, q_loads & 1)) break;
+      ++q_loads;
+      bool had0 = false, had1 = false, begun0 = false, begun1 = false;
+      for (int kt = first; ok && kt >= end - 1; --kt) {
+        const bool need0 = kt >= end && kt >= lo0 && kt < hi0, need1 = kt >= end && kt >= lo1 && kt < hi1;
+        if (!(need0 || need1) && !(had0 || had1)) continue;  // a gap between the two tiles' intervals
+        const int vslot = (ring + kRing - 1) % kRing, kslot = ring % kRing;
+        // one query tile's turn: P V of the key tile before, then S of this one
+        auto turn = [&](int q, bool had, bool need, bool& begun, int& pvs, int outs, bool frees_v, bool frees_k) {
+          const uint32_t tS = tm + q * 128, tO = tm + 256 + q * D;
+          if (had) {
+            if (!wait(bar_full + vslot, ((ring - 1) / kRing) & 1)) return;
+            // a new item's O overwrites the previous one's, which has to be read
+            if (!begun && outs > 0 && !wait(bar_o + q, (outs - 1) & 1)) return;
+            if (!wait(bar_p + q, pvs & 1)) return;
+            tc::fence_after();
+            const uint32_t b_lo = v_lo + vslot * (Lay::kTile >> 4);
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                tc::mma_f16_ts_words(tO, tS + 64 + kk * 8, b_lo + kk * 128, kHi, idPV, (begun[q] || kk > 0) ? 1u : 0u);
-              begun[q] = true;
+                tc::mma_f16_ts_words(tO, tS + 64 + kk * 8, b_lo + kk * 128, kHi, idPV, (begun || kk > 0) ? 1u : 0u);
               tc::commit(bar_pv + q);
-              ++pvs[q];
-              if (q == 1 || !had[1]) tc::commit(bar_empty + vslot);
+              if (frees_v) tc::commit(bar_empty + vslot);
             }
-            if (ok && need[q]) {
-              if (!k_seen) ok = mbar_wait_bounded(bar_full + kslot, (ring / kRing) & 1);
-              k_seen = true;
-              // S overwrites the tile's last P, whose product must be done
-              if (pvs[q] > 0) ok = ok && mbar_wait_bounded(bar_pv + q, (pvs[q] - 1) & 1);
-              if (!ok) break;
-              tc::fence_after();
-              const uint32_t a_lo = q_lo + q * (Lay::kTile >> 4), b_lo = k_lo + kslot * (Lay::kTile >> 4);
+            begun = true;
+            ++pvs;
+          }
+          if (need) {
+            if (!wait(bar_full + kslot, (ring / kRing) & 1)) return;
+            // S overwrites the tile's last P, whose product must be done
+            if (pvs > 0 && !wait(bar_pv + q, (pvs - 1) & 1)) return;
+            tc::fence_after();
+            const uint32_t a_lo = q_lo + q * (Lay::kTile >> 4), b_lo = k_lo + kslot * (Lay::kTile >> 4);
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * Lay::kSlab + (kk & 3) * 32) >> 4;  // 64-dim slab, 16-dim step
@@ -403,24 +445,27 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                 else tc::mma_f16_words<true>(tS, a_lo + off, kHi, b_lo + off, kHi, idS);
               }
               tc::commit(bar_s + q);
-              if (q == 1 || !need[1]) {
+              if (frees_k) {
                 tc::commit(bar_empty + kslot);
-                if (kt == kt_lo) tc::commit(bar_qempty);  // the item's last S
+                if (kt == end) tc::commit(bar_qempty);  // the item's last S
               }
             }
           }
-          had[0] = need[0];
-          had[1] = need[1];
-          if (any) ring += 2;
-        }
-        outs[0] += it.tile_lo[0] < it.tile_hi[0];
-        outs[1] += it.tile_lo[1] < it.tile_hi[1];
+        };
+        turn(0, had0, need0, begun0, pvs0, outs0, !had1, !need1);
+        if (ok) turn(1, had1, need1, begun1, pvs1, outs1, true, true);
+        had0 = need0;
+        had1 = need1;
+        if (need0 || need1) ring += 2;
       }
-      if (!ok) {  // a wait ran out: what was issued ends before the tensor memory goes
-        tc::commit(bar_end);
-        mbar_wait_bounded(bar_end, 0);
-      }
+      outs0 += lo0 < hi0;
+      outs1 += lo1 < hi1;
     }
+    if (!ok && leader) {  // a wait ran out: what was issued ends before the tensor memory goes
+      tc::commit(bar_end);
+      rl_wait(bar_end, 0);
+    }
+    __syncwarp();
   } else {
     // ---- softmax of query tile q: thread t of the tile's warps w and w + 4 has
     // row 32 w + t, the first its keys 0-63 and the second its keys 64-127
@@ -441,16 +486,19 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     for (int k = 0;; ++k) {
       const int slot = k & 1;
       // a row's two warps go on together: a wait that ran out for a lane of either ends both
-      if (barrier_or(pair, 64, !(ok && mbar_wait_bounded(bar_item + slot, (k >> 1) & 1)))) break;
-      const RlItem it = items[slot];
+      if (barrier_or(pair, 64, !(ok && rl_wait(bar_item + slot, (k >> 1) & 1)))) break;
+      const RlSpan walk(items[slot], q);
+      const bool last = items[slot].seq < 0;
+      const int t = items[slot].tok0 + tok;
+      const bool real = t < items[slot].n;
+      const int pos = items[slot].ctx + t, head = items[slot].head0 + hh, len = items[slot].len;
+      const int key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
+      const int64_t row = static_cast<int64_t>(items[slot].q_row) + t;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_free + slot);
-      if (it.seq < 0) break;
-      const int t = it.tok0 + tok;
-      const bool real = t < it.n;
-      const int pos = it.ctx + t, head = it.head0 + hh;
+      if (last) break;
       KeySpan span{0, 0};
-      if (real) span = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, pos, it.len);
+      if (real) span = keys_seen(p.rules, row, pos, len);
       float slope = 0.f;
       if constexpr (BIAS) slope = __ldg(p.rules.slopes + head) * kLog2e;
       // Weights and sums are relative to m_ref, the largest score of the first
@@ -458,13 +506,13 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // only when a tile's weights sum to more than kGrown.
       float m_ref = 0.f, l = 0.f;
       bool set = false, begun = false;
-      int ring = it.ring0;
-      for (int kt = (it.key_hi + kTcKeys - 1) / kTcKeys - 1; kt >= it.key_lo / kTcKeys; --kt) {
-        if (!rl_needs(it, 0, kt) && !rl_needs(it, 1, kt)) continue;
+      int ring = walk.ring0;
+      for (int kt = walk.first; kt >= walk.end; --kt) {
+        if (!walk.any(kt)) continue;
         ring += 2;
-        if (!rl_needs(it, q, kt)) continue;
+        if (!walk.own(kt)) continue;
         // after a timeout (recorded) the remaining waits are skipped
-        if (ok && !mbar_wait_bounded(bar_s + q, scores & 1)) ok = false;
+        if (ok && !rl_wait(bar_s + q, scores & 1)) ok = false;
         ++scores;
         tc::fence_after();
         const int k0 = kt * kTcKeys + 64 * half;  // this half's first key
@@ -534,7 +582,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                   x.x = in0 ? x.x : 0.f;
                   x.y = in1 ? x.y : 0.f;
                 }
-                const uint64_t d = tc::f2(x.x, x.y), z = tc::fmul2(d, cap.arg), u = tc::fmul2(z, z);
+                const uint64_t d = tc::f2(x.x, x.y), u = tc::fmul2(d, d);
                 const float2 u2 = tc::f2_split(u);
                 big = max3(big, u2.x, u2.y);
                 uint64_t y = tc::ffma2(cap.c[5], u, cap.c[4]);
@@ -557,7 +605,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
             }
           }
           sum = s0 + s1;
-          return CAP && !kExact && __any_sync(0xffffffffu, big > 1.f);
+          return CAP && !kExact && __any_sync(0xffffffffu, big > cap.limit);
         };
         auto weigh = [&]() {
           using std::false_type;
@@ -606,10 +654,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         tc::st_32x32b_x32(tS + 64 + 32 * half, pk);
         l += sum;
         // V rows z0 .. z1 - 1 have a weight somewhere
-        const int z0 = max(it.key_lo - kt * kTcKeys, 0), z1 = min(it.key_hi - kt * kTcKeys, kTcKeys);
+        const int z0 = max(key_lo - kt * kTcKeys, 0), z1 = min(key_hi - kt * kTcKeys, kTcKeys);
         if (z0 > 0 || z1 < kTcKeys) {
           const int vr = ring - 1;  // (both tiles' warps clear the same rows, each before its own P V)
-          if (ok && !mbar_wait_bounded(bar_full + vr % kRing, (vr / kRing) & 1)) ok = false;
+          if (ok && !rl_wait(bar_full + vr % kRing, (vr / kRing) & 1)) ok = false;
           uint8_t* vt = sm + Lay::kOffRing + (vr % kRing) * Lay::kTile;
 #pragma unroll 1
           for (int i = half * kTcRows + r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += 2 * kTcRows) {
@@ -626,7 +674,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + q);
       }
-      T* orow = static_cast<T*>(p.out) + (static_cast<int64_t>(it.q_row + t) * p.num_heads + head) * D + half * (D / 2);
+      T* orow = static_cast<T*>(p.out) + (row * p.num_heads + head) * D + half * (D / 2);
       if (!begun) {  // the tile sees no key
         if (real)
           for (int oc = 0; oc < D / 2; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
@@ -636,7 +684,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       named_barrier_sync(pair, 64);
       l += *row_other;
       named_barrier_sync(pair, 64);
-      if (ok && !mbar_wait_bounded(bar_pv + q, (scores - 1) & 1)) ok = false;
+      if (ok && !rl_wait(bar_pv + q, (scores - 1) & 1)) ok = false;
       tc::fence_after();
       const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
 #pragma unroll 1
