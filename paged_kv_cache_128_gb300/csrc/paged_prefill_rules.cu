@@ -32,8 +32,8 @@ namespace {
 // a column, over the upper half of its S), O at 256 and 256 + D.
 //   warp 17, scheduler and TMA producer: works out an item's ranges, hands them
 //     to the others through a two-deep ring in shared memory, and loads Q and
-//     the K and V tiles (one box per block and 64-dim slab, a lane each) into a
-//     ring of tile slots, running ahead into the next item;
+//     the K tiles (one box per block and 64-dim slab, a lane each) into a ring of
+//     slots, running ahead into the next item; warp 18 does so for the V tiles;
 //   warp 16 issues, for each key tile and for the two query tiles in turn, O +=
 //     P V of the previous key tile and S = Q K^T of this one (a warp for each
 //     query tile was slower, 558 us for 500: their MMAs interleave, both softmaxes
@@ -43,8 +43,8 @@ namespace {
 // V rows that lie in no row's interval are cleared before P V reads them.
 // ---------------------------------------------------------------------------
 constexpr int kRlSoftWarps = 8;  // per query tile: a row's keys are halved between two warps
-constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1;
-constexpr int kRlThreads = 32 * (kRlTmaWarp + 1);
+constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1, kRlValueWarp = kRlTmaWarp + 1;
+constexpr int kRlThreads = 32 * (kRlValueWarp + 1);
 constexpr uint32_t kRlCols = 512;
 
 // mbar_wait_bounded with the wait itself out of line: the many waits of this
@@ -56,7 +56,8 @@ __device__ __forceinline__ bool rl_wait(uint64_t* bar, uint32_t parity) {
 
 template <int D>
 struct RlLayout {
-  static constexpr int kRing = D == 64 ? 8 : 4;      // K and V tile slots
+  static constexpr int kDeep = D == 64 ? 4 : 2;      // slots for K tiles, and for V tiles
+  static constexpr int kRing = 2 * kDeep;            // tile n: K in slot n % kDeep, V kDeep further on
   static constexpr int kSlab = kTcRows * 128;        // one 64-column slab of 128 rows
   static constexpr int kTile = (D / 64) * kSlab;     // a Q, K or V tile
   static constexpr int kOffRing = 2 * kTile;         // after the two Q tiles
@@ -74,19 +75,24 @@ struct RlItem {
   int tok0, head0;  // first chunk token of the pair, first head of the group
   int key_lo, key_hi;          // keys that some row of the pair sees
   int tile_lo[2], tile_hi[2];  // key tiles of each query tile (none: equal)
-  int ring0;                   // ring position of the item's first K tile
+  int tile0;                   // tiles before the item's first
 };
 
 // The key tiles of an item as they are walked: first down to end, of which
 // own() says whether query tile q needs one, other() whether the other one does.
 struct RlSpan {
-  int first, end, own_lo, own_hi, other_lo, other_hi, ring0;
+  int first, end, own_lo, own_hi, other_lo, other_hi, tile0;
   __device__ __forceinline__ RlSpan(const RlItem& it, int q)
       : first((it.key_hi + kTcKeys - 1) / kTcKeys - 1), end(it.key_lo / kTcKeys), own_lo(it.tile_lo[q]),
-        own_hi(it.tile_hi[q]), other_lo(it.tile_lo[q ^ 1]), other_hi(it.tile_hi[q ^ 1]), ring0(it.ring0) {}
+        own_hi(it.tile_hi[q]), other_lo(it.tile_lo[q ^ 1]), other_hi(it.tile_hi[q ^ 1]), tile0(it.tile0) {}
   __device__ __forceinline__ bool own(int kt) const { return kt >= own_lo && kt < own_hi; }
   __device__ __forceinline__ bool other(int kt) const { return kt >= other_lo && kt < other_hi; }
   __device__ __forceinline__ bool any(int kt) const { return own(kt) || other(kt); }
+  __device__ __forceinline__ int below(int kt) const {  // the next tile down that either query tile needs
+    do --kt;
+    while (kt >= end && !any(kt));
+    return kt;
+  }
 };
 
 // The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     prefill_rules_kernel(const RulesPrefillParams p, const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using Lay = RlLayout<D>;
-  constexpr int kSlabs = D / 64, kRing = Lay::kRing;
+  constexpr int kSlabs = D / 64, kRing = Lay::kRing, kDeep = Lay::kDeep;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t rl_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rl_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   uint64_t* bar_pv = bar_p + 2;                 // [2] P V done
   uint64_t* bar_o = bar_pv + 2;                 // [2] O read (one arrival per softmax warp)
   uint64_t* bar_item = bar_o + 2;               // [2] item slot filled
-  uint64_t* bar_free = bar_item + 2;            // [2] item slot read (MMA warp and every softmax warp)
+  uint64_t* bar_free = bar_item + 2;            // [2] item slot read (MMA, V and softmax warps)
   uint64_t* bar_end = bar_free + 2;             // after a wait ran out: all MMAs done
   RlItem* items = reinterpret_cast<RlItem*>(bar_end + 1);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       mbar_init(bar_pv + i, 1);
       mbar_init(bar_o + i, kRlSoftWarps);
       mbar_init(bar_item + i, 1);
-      mbar_init(bar_free + i, 1 + 2 * kRlSoftWarps);
+      mbar_init(bar_free + i, 2 + 2 * kRlSoftWarps);
     }
     mbar_init(bar_end, 1);
     fence_mbar_init();
@@ -202,11 +208,13 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kRlTmaWarp) {
-    // ---- scheduler and TMA producer (the whole warp)
-    const int ngroups = p.num_heads >> p.hg_log2;
-    const int64_t total = static_cast<int64_t>(ngroups) * p.num_seqs * p.row_tiles;
-    int ring = 0, armed = 0, handed = 0, q_loads = 0, k_tiles = 0;
+  if (warp >= kRlTmaWarp) {
+    // ---- TMA producers: one warp schedules and loads Q and K, the other V (a
+    // copy per block and slab is issued at a time, so that one warp took longer
+    // over the 32 copies of a K and a V tile of 16-token blocks than the tensor
+    // cores over their products: 481 us, and 436 with two)
+    const bool values = warp == kRlValueWarp;
+    int loaded = 0;  // tiles
     bool ok = true;
     // a wait by lane 0 for the whole warp
     auto wait = [&](uint64_t* bar, int parity) {
@@ -215,159 +223,179 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       ok = __shfl_sync(0xffffffffu, w, 0) != 0;
       return ok;
     };
-    auto hand_on = [&](const RlItem& it) {
-      const int slot = handed & 1;
-      if (handed >= 2 && !wait(bar_free + slot, ((handed >> 1) - 1) & 1)) return;
-      if (lane == 0) {
-        items[slot] = it;
-        mbar_arrive(bar_item + slot);
+    // This lane's copy of a tile: slab lane % kSlabs of its block lane / kSlabs;
+    // a tile has the blocks that hold keys key_lo .. key_hi - 1.
+    const int my_blk = lane / kSlabs, my_slab = lane % kSlabs;
+    // table entry of this lane's block in tile kt (-1: none)
+    auto entry = [&](int seq, int key_lo, int key_hi, int kt) {
+      const int blk = kt * (kTcKeys / bs) + my_blk;
+      const bool in = my_blk < kTcKeys / bs && (blk + 1) * static_cast<int64_t>(bs) > key_lo &&
+                      static_cast<int64_t>(blk) * bs < key_hi;
+      int e = -1;
+      if (in) {
+        e = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
+        if (e < 0 || e >= p.num_blocks) {
+          record_error(KV_ERR_DEVICE_BOUNDS);
+          e = 0;
+        }
       }
-      ++handed;
+      return e;
     };
-    // Items come in order of falling length (row tiles counted down); every
-    // other round of CTAs takes them in reverse, so that the sums even out.
-    for (int64_t round = 0; round * gridDim.x < total && ok; ++round) {
-      const int64_t x = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      if (x >= total) continue;
-      const int gi = static_cast<int>(x % ngroups);
-      const int b = static_cast<int>((x / ngroups) % p.num_seqs);
-      const int pair = p.row_tiles - 1 - static_cast<int>(x / ngroups / p.num_seqs);
-      RlItem it;
-      it.seq = b;
-      it.q_row = __ldg(p.query_start + b);
-      it.n = __ldg(p.query_start + b + 1) - it.q_row;
-      it.tok0 = pair * 2 * tpt;
-      it.head0 = gi * hg;
-      // rows past the grid's reach (a chunk longer than max_query_len) would be
-      // left uncomputed: the sequence's last pair reports it
-      if (pair == p.row_tiles - 1 && gi == 0 && lane == 0 && it.n > p.row_tiles * 2 * static_cast<int64_t>(tpt))
-        record_error(KV_ERR_DEVICE_BOUNDS);
-      if (it.n <= 0 || it.tok0 >= it.n) continue;
-      it.len = __ldg(p.seq_lens + b);
-      const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
-      // the chunk must lie inside its sequence and in q, the sequence in its table row
-      if (it.len < it.n || it.q_row < 0 || it.q_row + static_cast<int64_t>(it.n) > p.num_tokens) {
-        if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
-        continue;
+    auto load = [&](const CUtensorMap* map, int kvh, int e) {
+      const int slot = (values ? kDeep : 0) + loaded % kDeep;
+      if (loaded >= kDeep && !wait(bar_empty + slot, ((loaded / kDeep) - 1) & 1)) return;
+      if (!values && p.test_skip >= 0 && blockIdx.x == 0 && loaded == p.test_skip) {
+        ok = false;  // test control: this tile never lands, and none after it
+        return;
       }
-      if (it.len > cap) {
-        if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
-        it.len = static_cast<int>(cap);
-        if (it.len < it.n) continue;
-      }
-      it.ctx = it.len - it.n;
-      it.key_lo = INT32_MAX;
-      it.key_hi = 0;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
-        int lo = INT32_MAX, hi = 0;
-        if (p.rules.key_begin || p.rules.key_end) {
-          for (int t = t0 + lane; t < t1; t += 32) {
-            const KeySpan s = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, it.ctx + t, it.len);
-            if (s.lo < s.hi) {
-              lo = min(lo, s.lo);
-              hi = max(hi, s.hi);
-            }
-          }
-          lo = __reduce_min_sync(0xffffffffu, lo);
-          hi = __reduce_max_sync(0xffffffffu, hi);
-        } else if (t0 < t1) {  // a window's ends move with the row
-          lo = keys_seen(p.rules, 0, it.ctx + t0, it.len).lo;
-          hi = keys_seen(p.rules, 0, it.ctx + t1 - 1, it.len).hi;
-        }
-        it.tile_lo[q] = lo < hi ? lo / kTcKeys : 0;
-        it.tile_hi[q] = lo < hi ? (hi + kTcKeys - 1) / kTcKeys : 0;
-        if (lo < hi) {
-          it.key_lo = min(it.key_lo, lo);
-          it.key_hi = max(it.key_hi, hi);
-        }
-      }
-      it.ring0 = ring;
-      hand_on(it);
-      if (!ok || it.key_lo >= it.key_hi) continue;
-      const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-      const int kvh = it.head0 / p.group;
-      // This lane's copy of a tile: slab lane % kSlabs of its block lane /
-      // kSlabs; a tile has the blocks that hold keys key_lo .. key_hi - 1.
-      const int my_blk = lane / kSlabs, my_slab = lane % kSlabs;
-      auto entry = [&](int kt) {  // table entry of this lane's block in tile kt (-1: none)
-        const int blk = kt * (kTcKeys / bs) + my_blk;
-        const bool in = my_blk < kTcKeys / bs && (blk + 1) * static_cast<int64_t>(bs) > it.key_lo &&
-                        static_cast<int64_t>(blk) * bs < it.key_hi;
-        int e = -1;
-        if (in) {
-          e = __ldg(table + blk);
-          if (e < 0 || e >= p.num_blocks) {
-            record_error(KV_ERR_DEVICE_BOUNDS);
-            e = 0;
-          }
-        }
-        return e;
-      };
-      auto load = [&](int kt, int e, bool is_v) {
-        const int slot = ring % kRing;
-        if (ring >= kRing && !wait(bar_empty + slot, ((ring / kRing) - 1) & 1)) return;
-        const bool skip = !is_v && p.test_skip >= 0 && blockIdx.x == 0 && k_tiles == p.test_skip;
-        if (!is_v) ++k_tiles;
-        if (skip) {
-          ok = false;  // test control: this tile never lands, and none after it
-          return;
-        }
-        const int copies = __popc(__ballot_sync(0xffffffffu, e >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(bar_full + slot, static_cast<uint32_t>(copies * bs * 128));
+      const int copies = __popc(__ballot_sync(0xffffffffu, e >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(bar_full + slot, static_cast<uint32_t>(copies * bs * 128));
+      __syncwarp();
+      if (e >= 0)
+        tma_load_3d(sm + Lay::kOffRing + slot * Lay::kTile + my_slab * Lay::kSlab + my_blk * bs * 128, map,
+                    bar_full + slot, my_slab * 64, kvh, e * bs);
+      ++loaded;
+    };
+    int q_loads = 0;
+    if (values) {
+      for (int k = 0;; ++k) {
+        const int slot = k & 1;
+        if (!wait(bar_item + slot, (k >> 1) & 1)) break;
+        const RlSpan walk(items[slot], 0);
+        const int seq = items[slot].seq, key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
+        const int kvh = items[slot].head0 / p.group;
         __syncwarp();
-        if (e >= 0)
-          tma_load_3d(sm + Lay::kOffRing + slot * Lay::kTile + my_slab * Lay::kSlab + my_blk * bs * 128,
-                      is_v ? &tmV : &tmK, bar_full + slot, my_slab * 64, kvh, e * bs);
-        armed = ++ring;
-      };
-      const RlSpan walk(it, 0);
-      const int kt_lo = walk.end;
-      auto below = [&](int kt) {  // the next tile down that either query tile needs
-        do --kt;
-        while (kt >= kt_lo && !walk.any(kt));
-        return kt;
-      };
-      int kt = below(walk.first + 1);
-      int e = entry(kt);
-      bool first = true;
-      while (kt >= kt_lo && ok) {
-        load(kt, e, false);
-        if (first && ok) {  // Q after the first K tile, which waits for less
-          first = false;
-          if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar_qfull, 2 * Lay::kTile);
-            for (int q = 0; q < 2; ++q)
-              for (int s = 0; s < kSlabs; ++s)
-                tma_load_3d(sm + q * Lay::kTile + s * Lay::kSlab, &tmQ, bar_qfull, s * 64, it.head0,
-                            it.q_row + it.tok0 + q * tpt);
-          }
-          ++q_loads;
+        if (lane == 0) mbar_arrive(bar_free + slot);
+        if (seq < 0) break;
+        int kt = walk.below(walk.first + 1);
+        int e = kt >= walk.end ? entry(seq, key_lo, key_hi, kt) : -1;
+        while (kt >= walk.end && ok) {
+          const int next = walk.below(kt);
+          const int e_next = next >= walk.end ? entry(seq, key_lo, key_hi, next) : -1;
+          load(&tmV, kvh, e);
+          kt = next;
+          e = e_next;
         }
-        const int next = below(kt);
-        const int e_next = next >= kt_lo ? entry(next) : -1;
-        if (ok) load(kt, e, true);
-        kt = next;
-        e = e_next;
+        if (!ok) break;
+      }
+    } else {
+      const int ngroups = p.num_heads >> p.hg_log2;
+      const int64_t total = static_cast<int64_t>(ngroups) * p.num_seqs * p.row_tiles;
+      int handed = 0;
+      auto hand_on = [&](const RlItem& it) {
+        const int slot = handed & 1;
+        if (handed >= 2 && !wait(bar_free + slot, ((handed >> 1) - 1) & 1)) return;
+        if (lane == 0) {
+          items[slot] = it;
+          mbar_arrive(bar_item + slot);
+        }
+        ++handed;
+      };
+      // Items come in order of falling length (row tiles counted down); every
+      // other round of CTAs takes them in reverse, so that the sums even out.
+      for (int64_t round = 0; round * gridDim.x < total && ok; ++round) {
+        const int64_t x = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if (x >= total) continue;
+        const int gi = static_cast<int>(x % ngroups);
+        const int b = static_cast<int>((x / ngroups) % p.num_seqs);
+        const int pair = p.row_tiles - 1 - static_cast<int>(x / ngroups / p.num_seqs);
+        RlItem it;
+        it.seq = b;
+        it.q_row = __ldg(p.query_start + b);
+        it.n = __ldg(p.query_start + b + 1) - it.q_row;
+        it.tok0 = pair * 2 * tpt;
+        it.head0 = gi * hg;
+        // rows past the grid's reach (a chunk longer than max_query_len) would be
+        // left uncomputed: the sequence's last pair reports it
+        if (pair == p.row_tiles - 1 && gi == 0 && lane == 0 && it.n > p.row_tiles * 2 * static_cast<int64_t>(tpt))
+          record_error(KV_ERR_DEVICE_BOUNDS);
+        if (it.n <= 0 || it.tok0 >= it.n) continue;
+        it.len = __ldg(p.seq_lens + b);
+        const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+        // the chunk must lie inside its sequence and in q, the sequence in its table row
+        if (it.len < it.n || it.q_row < 0 || it.q_row + static_cast<int64_t>(it.n) > p.num_tokens) {
+          if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
+          continue;
+        }
+        if (it.len > cap) {
+          if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
+          it.len = static_cast<int>(cap);
+          if (it.len < it.n) continue;
+        }
+        it.ctx = it.len - it.n;
+        it.key_lo = INT32_MAX;
+        it.key_hi = 0;
+  #pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
+          int lo = INT32_MAX, hi = 0;
+          if (p.rules.key_begin || p.rules.key_end) {
+            for (int t = t0 + lane; t < t1; t += 32) {
+              const KeySpan s = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, it.ctx + t, it.len);
+              if (s.lo < s.hi) {
+                lo = min(lo, s.lo);
+                hi = max(hi, s.hi);
+              }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+          } else if (t0 < t1) {  // a window's ends move with the row
+            lo = keys_seen(p.rules, 0, it.ctx + t0, it.len).lo;
+            hi = keys_seen(p.rules, 0, it.ctx + t1 - 1, it.len).hi;
+          }
+          it.tile_lo[q] = lo < hi ? lo / kTcKeys : 0;
+          it.tile_hi[q] = lo < hi ? (hi + kTcKeys - 1) / kTcKeys : 0;
+          if (lo < hi) {
+            it.key_lo = min(it.key_lo, lo);
+            it.key_hi = max(it.key_hi, hi);
+          }
+        }
+        it.tile0 = loaded;
+        hand_on(it);
+        if (!ok || it.key_lo >= it.key_hi) continue;
+        const int kvh = it.head0 / p.group;
+        const RlSpan walk(it, 0);
+        int kt = walk.below(walk.first + 1);
+        int e = entry(b, it.key_lo, it.key_hi, kt);
+        bool first = true;
+        while (kt >= walk.end && ok) {
+          const int next = walk.below(kt);
+          const int e_next = next >= walk.end ? entry(b, it.key_lo, it.key_hi, next) : -1;
+          load(&tmK, kvh, e);
+          if (first && ok) {  // Q after the first K tile, which waits for less
+            first = false;
+            if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar_qfull, 2 * Lay::kTile);
+              for (int q = 0; q < 2; ++q)
+                for (int s = 0; s < kSlabs; ++s)
+                  tma_load_3d(sm + q * Lay::kTile + s * Lay::kSlab, &tmQ, bar_qfull, s * 64, it.head0,
+                              it.q_row + it.tok0 + q * tpt);
+            }
+            ++q_loads;
+          }
+          kt = next;
+          e = e_next;
+        }
+      }
+      if (ok) {
+        RlItem stop;
+        stop.seq = -1;
+        hand_on(stop);
       }
     }
-    if (ok) {
-      RlItem stop;
-      stop.seq = -1;
-      hand_on(stop);
-    }
-    // At exit no copy or commit is in flight: the ring's last tiles have been
+    // At exit no copy or commit is in flight: the warp's last tiles have been
     // read, or, where a wait ran out, their copies have at least landed.
     __syncwarp();
     if (lane == 0) {
+      uint64_t* const full = bar_full + (values ? kDeep : 0);
+      uint64_t* const empty = bar_empty + (values ? kDeep : 0);
       bool drained = ok;
-      if (drained) drained = drain_fills(bar_empty, armed, kRing, false);
+      if (drained) drained = drain_fills(empty, loaded, kDeep, false);
       if (drained && q_loads > 0) drained = rl_wait(bar_qempty, (q_loads - 1) & 1);
       if (!drained) {
         if (q_loads > 0) rl_wait(bar_qfull, (q_loads - 1) & 1);
-        drain_fills(bar_full, armed, kRing, true);
+        drain_fills(full, loaded, kDeep, true);
       }
     }
   } else if (warp == kRlMmaWarp) {
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     };
     int q_loads = 0, pvs0 = 0, pvs1 = 0;  // Q loads, P V products
     int outs0 = 0, outs1 = 0;             // items with an output
-    int ring = 0;  // of this step's K tile; its V is the next, the previous step's V the one before
+    int n = 0;                            // tiles before this step's
     for (int k = 0; ok; ++k) {
       const int slot = k & 1;
       if (!wait(bar_item + slot, (k >> 1) & 1)) break;
@@ -410,12 +438,12 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       for (int kt = first; ok && kt >= end - 1; --kt) {
         const bool need0 = kt >= end && kt >= lo0 && kt < hi0, need1 = kt >= end && kt >= lo1 && kt < hi1;
         if (!(need0 || need1) && !(had0 || had1)) continue;  // a gap between the two tiles' intervals
-        const int vslot = (ring + kRing - 1) % kRing, kslot = ring % kRing;
+        const int vslot = kDeep + (n + kDeep - 1) % kDeep, kslot = n % kDeep;  // V of the tile before, K of this one
         // one query tile's turn: P V of the key tile before, then S of this one
         auto turn = [&](int q, bool had, bool need, bool& begun, int& pvs, int outs, bool frees_v, bool frees_k) {
           const uint32_t tS = tm + q * 128, tO = tm + 256 + q * D;
           if (had) {
-            if (!wait(bar_full + vslot, ((ring - 1) / kRing) & 1)) return;
+            if (!wait(bar_full + vslot, ((n - 1) / kDeep) & 1)) return;
             // a new item's O overwrites the previous one's, which has to be read
             if (!begun && outs > 0 && !wait(bar_o + q, (outs - 1) & 1)) return;
             if (!wait(bar_p + q, pvs & 1)) return;
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
             ++pvs;
           }
           if (need) {
-            if (!wait(bar_full + kslot, (ring / kRing) & 1)) return;
+            if (!wait(bar_full + kslot, (n / kDeep) & 1)) return;
             // S overwrites the tile's last P, whose product must be done
             if (pvs > 0 && !wait(bar_pv + q, (pvs - 1) & 1)) return;
             tc::fence_after();
@@ -456,7 +484,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         if (ok) turn(1, had1, need1, begun1, pvs1, outs1, true, true);
         had0 = need0;
         had1 = need1;
-        if (need0 || need1) ring += 2;
+        if (need0 || need1) ++n;
       }
       outs0 += lo0 < hi0;
       outs1 += lo1 < hi1;
@@ -506,10 +534,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // only when a tile's weights sum to more than kGrown.
       float m_ref = 0.f, l = 0.f;
       bool set = false, begun = false;
-      int ring = walk.ring0;
+      int n = walk.tile0;  // tiles up to and with this one
       for (int kt = walk.first; kt >= walk.end; --kt) {
         if (!walk.any(kt)) continue;
-        ring += 2;
+        ++n;
         if (!walk.own(kt)) continue;
         // after a timeout (recorded) the remaining waits are skipped
         if (ok && !rl_wait(bar_s + q, scores & 1)) ok = false;
@@ -656,9 +684,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         // V rows z0 .. z1 - 1 have a weight somewhere
         const int z0 = max(key_lo - kt * kTcKeys, 0), z1 = min(key_hi - kt * kTcKeys, kTcKeys);
         if (z0 > 0 || z1 < kTcKeys) {
-          const int vr = ring - 1;  // (both tiles' warps clear the same rows, each before its own P V)
-          if (ok && !rl_wait(bar_full + vr % kRing, (vr / kRing) & 1)) ok = false;
-          uint8_t* vt = sm + Lay::kOffRing + (vr % kRing) * Lay::kTile;
+          // (both tiles' warps clear the same rows, each before its own P V)
+          const int vslot = kDeep + (n - 1) % kDeep;
+          if (ok && !rl_wait(bar_full + vslot, ((n - 1) / kDeep) & 1)) ok = false;
+          uint8_t* vt = sm + Lay::kOffRing + vslot * Lay::kTile;
 #pragma unroll 1
           for (int i = half * kTcRows + r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += 2 * kTcRows) {
             const int row = i / (kSlabs * 8), rest = i % (kSlabs * 8);
