@@ -552,27 +552,52 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         const uint32_t tSh = tS + 64 * half;
         uint32_t pk[32];  // P, two keys to a column
         float sum;
-        // The half's largest score, over the row with the other warp's.
+        // The row's largest score, over both halves.  The cap grows with the
+        // score, so that without a bias it is taken of the largest alone; with one,
+        // every score is capped, by the polynomial unless one lies beyond it.
         auto row_max = [&]() {
           float m = -INFINITY;
+          auto scan = [&](auto in_full) -> bool {
+            constexpr bool kExact = decltype(in_full)::value;
+            float big = 0.f;
+            m = -INFINITY;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            uint32_t s[32];
-            tc::ld_32x32b_x32(tSh + c0, s);
-            tc::wait_ld();
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              uint32_t s[32];
+              tc::ld_32x32b_x32(tSh + c0, s);
+              tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = c0 + i;
-              float x = __uint_as_float(s[i]);
-              x = CAP ? soft_cap(x, c2, p.rules.cap_log2, p.rules.cap_arg) : x * c2;
-              if (BIAS) x = fmaf(-slope, fabsf(ahead - c), x);
-              if (c >= lo && c < hi) m = fmaxf(m, x);
+              for (int i = 0; i < 32; ++i) {
+                const int c = c0 + i;
+                const float d = c >= lo && c < hi ? __uint_as_float(s[i]) : NAN;  // fmaxf passes a NaN over
+                float x = d * c2;
+                if constexpr (CAP && BIAS) {
+                  if constexpr (kExact) {
+                    x = soft_cap(d, c2, p.rules.cap_log2, p.rules.cap_arg);
+                  } else {
+                    const float u = d * d;
+                    big = fmaxf(big, u);
+                    float y = fmaf(tc::f2_split(cap.c[5]).x, u, tc::f2_split(cap.c[4]).x);
+#pragma unroll
+                    for (int j = 3; j >= 0; --j) y = fmaf(y, u, tc::f2_split(cap.c[j]).x);
+                    x = d * y;
+                  }
+                }
+                if (BIAS) x = fmaf(-slope, fabsf(ahead - c), x);
+                m = fmaxf(m, x);
+              }
             }
+            return __any_sync(0xffffffffu, big > cap.limit);
+          };
+          if (scan(std::false_type())) {
+            if constexpr (CAP && BIAS) scan(std::true_type());
           }
           *row_own = m;
           named_barrier_sync(pair, 64);
           m = fmaxf(m, *row_other);
           named_barrier_sync(pair, 64);  // read before it is written again
+          if (CAP && !BIAS && m != -INFINITY)
+            m = soft_cap(m, 1.f, p.rules.cap_log2, __fdiv_rn(1.f, p.rules.cap_log2));
           return m;
         };
         // P = exp2(score - m_ref) rounded to T (keys the row does not see: 0), and
@@ -598,8 +623,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
               const bool in0 = !kPart || (c >= lo && c < hi), in1 = !kPart || (c + 1 >= lo && c + 1 < hi);
               uint64_t base = negm;
               if constexpr (BIAS) {
-                if (kPart) base = tc::f2(fmaf(-slope, fabsf(ahead - c), -m_ref), fmaf(-slope, fabsf(ahead - (c + 1)), -m_ref));
-                else base = tc::ffma2(sl2, tc::f2(2.f * i, 2.f * i + 1.f), b0x2);
+                if (kPart)
+                  base = tc::f2(fmaf(-slope, fabsf(ahead - c), -m_ref), fmaf(-slope, fabsf(ahead - (c + 1)), -m_ref));
+                else
+                  base = tc::ffma2(sl2, tc::f2(2.f * i, 2.f * i + 1.f), b0x2);
               }
               if constexpr (CAP && kExact) {
                 const float2 b = tc::f2_split(base);
