@@ -280,7 +280,6 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       }
     } else {
       const int ngroups = p.num_heads >> p.hg_log2;
-      const int64_t total = static_cast<int64_t>(ngroups) * p.num_seqs * p.row_tiles;
       int handed = 0;
       auto hand_on = [&](const RlItem& it) {
         const int slot = handed & 1;
@@ -291,92 +290,113 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         }
         ++handed;
       };
-      // Items come in order of falling length (row tiles counted down); every
-      // other round of CTAs takes them in reverse, so that the sums even out.
-      for (int64_t round = 0; round * gridDim.x < total && ok; ++round) {
-        const int64_t x = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (x >= total) continue;
-        const int gi = static_cast<int>(x % ngroups);
-        const int b = static_cast<int>((x / ngroups) % p.num_seqs);
-        const int pair = p.row_tiles - 1 - static_cast<int>(x / ngroups / p.num_seqs);
-        RlItem it;
-        it.seq = b;
-        it.q_row = __ldg(p.query_start + b);
-        it.n = __ldg(p.query_start + b + 1) - it.q_row;
-        it.tok0 = pair * 2 * tpt;
-        it.head0 = gi * hg;
-        // rows past the grid's reach (a chunk longer than max_query_len) would be
-        // left uncomputed: the sequence's last pair reports it
-        if (pair == p.row_tiles - 1 && gi == 0 && lane == 0 && it.n > p.row_tiles * 2 * static_cast<int64_t>(tpt))
-          record_error(KV_ERR_DEVICE_BOUNDS);
-        if (it.n <= 0 || it.tok0 >= it.n) continue;
-        it.len = __ldg(p.seq_lens + b);
-        const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
-        // the chunk must lie inside its sequence and in q, the sequence in its table row
-        if (it.len < it.n || it.q_row < 0 || it.q_row + static_cast<int64_t>(it.n) > p.num_tokens) {
-          if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
-          continue;
+      // Items in order: sequence by sequence, a sequence's pairs counted down
+      // (the longest first), head groups innermost.  CTA c takes items c, c +
+      // grid, ..., every other round in reverse, so that the sums even out.
+      // Sequences are looked at 32 at a time, a lane each, and once: what has
+      // no rows has no items, whatever max_query_len allows for.
+      int64_t round = 0, before = 0;  // items of the sequences before this chunk of 32
+      auto item_of = [&](int64_t r) {
+        return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      };
+      for (int b0 = 0; b0 < p.num_seqs && ok; b0 += 32) {
+        const int my_b = b0 + lane;
+        int my_row = 0, my_n = 0, my_len = 0;
+        if (my_b < p.num_seqs) {
+          my_row = __ldg(p.query_start + my_b);
+          my_n = __ldg(p.query_start + my_b + 1) - my_row;
+          my_len = __ldg(p.seq_lens + my_b);
+          const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+          // rows past the reach of max_query_len are left uncomputed; the chunk must
+          // lie inside its sequence and in q, the sequence in its table row
+          const bool bad =
+              my_n > 0 && (my_len < my_n || my_row < 0 || my_row + static_cast<int64_t>(my_n) > p.num_tokens);
+          if (blockIdx.x == 0 &&
+              (bad || (my_n > 0 && (my_n > p.row_tiles * 2 * static_cast<int64_t>(tpt) || my_len > cap))))
+            record_error(KV_ERR_DEVICE_BOUNDS);
+          if (my_len > cap) my_len = static_cast<int>(cap);
+          if (bad || my_len < my_n) my_n = 0;
         }
-        if (it.len > cap) {
-          if (lane == 0) record_error(KV_ERR_DEVICE_BOUNDS);
-          it.len = static_cast<int>(cap);
-          if (it.len < it.n) continue;
+        const int my_pairs = min(max(my_n, 0) / (2 * tpt) + (max(my_n, 0) % (2 * tpt) != 0), p.row_tiles);
+        int64_t upto = static_cast<int64_t>(my_pairs) * ngroups;  // items up to and with this lane's sequence
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
         }
-        it.ctx = it.len - it.n;
-        it.key_lo = INT32_MAX;
-        it.key_hi = 0;
-  #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
-          int lo = INT32_MAX, hi = 0;
-          if (p.rules.key_begin || p.rules.key_end) {
-            for (int t = t0 + lane; t < t1; t += 32) {
-              const KeySpan s = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, it.ctx + t, it.len);
-              if (s.lo < s.hi) {
-                lo = min(lo, s.lo);
-                hi = max(hi, s.hi);
+        upto += before;
+        const int64_t end = __shfl_sync(0xffffffffu, upto, 31);
+        for (; item_of(round) < end && ok; ++round) {
+          const int64_t x = item_of(round);
+          const int src = __ffs(__ballot_sync(0xffffffffu, x < upto)) - 1;  // the lane whose sequence x lies in
+          const int pairs = __shfl_sync(0xffffffffu, my_pairs, src);
+          const int64_t rel = x - (__shfl_sync(0xffffffffu, upto, src) - static_cast<int64_t>(pairs) * ngroups);
+          const int b = b0 + src, gi = static_cast<int>(rel % ngroups);
+          const int pair = pairs - 1 - static_cast<int>(rel / ngroups);
+          RlItem it;
+          it.seq = b;
+          it.q_row = __shfl_sync(0xffffffffu, my_row, src);
+          it.n = __shfl_sync(0xffffffffu, my_n, src);
+          it.len = __shfl_sync(0xffffffffu, my_len, src);
+          it.tok0 = pair * 2 * tpt;
+          it.head0 = gi * hg;
+          it.ctx = it.len - it.n;
+          it.key_lo = INT32_MAX;
+          it.key_hi = 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
+            int lo = INT32_MAX, hi = 0;
+            if (p.rules.key_begin || p.rules.key_end) {
+              for (int t = t0 + lane; t < t1; t += 32) {
+                const KeySpan s = keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t, it.ctx + t, it.len);
+                if (s.lo < s.hi) {
+                  lo = min(lo, s.lo);
+                  hi = max(hi, s.hi);
+                }
               }
+              lo = __reduce_min_sync(0xffffffffu, lo);
+              hi = __reduce_max_sync(0xffffffffu, hi);
+            } else if (t0 < t1) {  // a window's ends move with the row
+              lo = keys_seen(p.rules, 0, it.ctx + t0, it.len).lo;
+              hi = keys_seen(p.rules, 0, it.ctx + t1 - 1, it.len).hi;
             }
-            lo = __reduce_min_sync(0xffffffffu, lo);
-            hi = __reduce_max_sync(0xffffffffu, hi);
-          } else if (t0 < t1) {  // a window's ends move with the row
-            lo = keys_seen(p.rules, 0, it.ctx + t0, it.len).lo;
-            hi = keys_seen(p.rules, 0, it.ctx + t1 - 1, it.len).hi;
+            it.tile_lo[q] = lo < hi ? lo / kTcKeys : 0;
+            it.tile_hi[q] = lo < hi ? (hi + kTcKeys - 1) / kTcKeys : 0;
+            if (lo < hi) {
+              it.key_lo = min(it.key_lo, lo);
+              it.key_hi = max(it.key_hi, hi);
+            }
           }
-          it.tile_lo[q] = lo < hi ? lo / kTcKeys : 0;
-          it.tile_hi[q] = lo < hi ? (hi + kTcKeys - 1) / kTcKeys : 0;
-          if (lo < hi) {
-            it.key_lo = min(it.key_lo, lo);
-            it.key_hi = max(it.key_hi, hi);
+          it.tile0 = loaded;
+          hand_on(it);
+          if (!ok || it.key_lo >= it.key_hi) continue;
+          const int kvh = it.head0 / p.group;
+          const RlSpan walk(it, 0);
+          int kt = walk.below(walk.first + 1);
+          int e = entry(b, it.key_lo, it.key_hi, kt);
+          bool first = true;
+          while (kt >= walk.end && ok) {
+            const int next = walk.below(kt);
+            const int e_next = next >= walk.end ? entry(b, it.key_lo, it.key_hi, next) : -1;
+            load(&tmK, kvh, e);
+            if (first && ok) {  // Q after the first K tile, which waits for less
+              first = false;
+              if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(bar_qfull, 2 * Lay::kTile);
+                for (int q = 0; q < 2; ++q)
+                  for (int s = 0; s < kSlabs; ++s)
+                    tma_load_3d(sm + q * Lay::kTile + s * Lay::kSlab, &tmQ, bar_qfull, s * 64, it.head0,
+                                it.q_row + it.tok0 + q * tpt);
+              }
+              ++q_loads;
+            }
+            kt = next;
+            e = e_next;
           }
         }
-        it.tile0 = loaded;
-        hand_on(it);
-        if (!ok || it.key_lo >= it.key_hi) continue;
-        const int kvh = it.head0 / p.group;
-        const RlSpan walk(it, 0);
-        int kt = walk.below(walk.first + 1);
-        int e = entry(b, it.key_lo, it.key_hi, kt);
-        bool first = true;
-        while (kt >= walk.end && ok) {
-          const int next = walk.below(kt);
-          const int e_next = next >= walk.end ? entry(b, it.key_lo, it.key_hi, next) : -1;
-          load(&tmK, kvh, e);
-          if (first && ok) {  // Q after the first K tile, which waits for less
-            first = false;
-            if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar_qfull, 2 * Lay::kTile);
-              for (int q = 0; q < 2; ++q)
-                for (int s = 0; s < kSlabs; ++s)
-                  tma_load_3d(sm + q * Lay::kTile + s * Lay::kSlab, &tmQ, bar_qfull, s * 64, it.head0,
-                              it.q_row + it.tok0 + q * tpt);
-            }
-            ++q_loads;
-          }
-          kt = next;
-          e = e_next;
-        }
+        before = end;
       }
       if (ok) {
         RlItem stop;
