@@ -24,7 +24,8 @@ HEADERS = [os.path.join(ROOT, "include", "pagedkv.h"), os.path.join(CSRC, "commo
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CUDA_SOURCES = ["reshape_and_cache.cu", "paged_decode.cu", "paged_prefill.cu", "step_runner.cu",
-                "rope_and_cache.cu", "shared_prefix.cu", "paged_decode_rules.cu", "paged_prefill_rules.cu"]
+                "rope_and_cache.cu", "shared_prefix.cu", "paged_decode_rules.cu",
+                "paged_decode_rules_cap.cu", "paged_prefill_rules.cu"]
 CXX_SOURCES = ["block_manager.cpp"]
 
 

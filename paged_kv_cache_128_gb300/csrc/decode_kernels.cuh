@@ -54,6 +54,15 @@ namespace pagedkv {
 // Tag of one stream-K call (one counter for the library).
 uint64_t next_epoch();
 
+// The step's new tokens for paged_decode_step (null for attention alone).
+struct StepArgs {
+  const void* k;
+  const void* v;
+  const int32_t* slot_mapping;
+  const int32_t* new_token_row;
+  int64_t num_tokens, k_stride, v_stride;  // strides in elements
+};
+
 namespace {
 
 struct DecodeParams {
@@ -92,10 +101,13 @@ struct DecodeParams {
   const float* v_scales;
 };
 
-// The same with score rules (score_rules.cuh); the kernels are compiled for
-// either.
+// The same with score rules (score_rules.cuh), with and without a cap; the
+// kernels are compiled for each of the three.  (With the cap's test at run time
+// the fp8 kernel was a quarter slower without one, 194 us for 136: its code no
+// longer stayed in the instruction cache.)
+template <bool CAP>
 struct RulesParams : DecodeParams {
-  static constexpr bool kRules = true;
+  static constexpr bool kRules = true, kCap = CAP;
   ScoreRules rules;
 };
 
@@ -127,18 +139,17 @@ __device__ __forceinline__ int first_key(const P& p, int b, int L) {
 template <int NG, typename P>
 __device__ __forceinline__ auto tile_rules(const P& p, int kvh, int L, int lo, int lane) {
   if constexpr (P::kRules) {
-    TileRules<NG> r;
+    TileRules<NG, P::kCap> r;
     r.cap_log2 = p.rules.cap_log2;
     r.cap_arg = p.rules.cap_arg;
     r.lo = lo;
     r.pos = L - 1;
 #pragma unroll
-    for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int g = ng * 8 + (lane & 3) * 2 + c;
-        r.slope[ng][c] = p.rules.slopes && g < p.group ? __ldg(p.rules.slopes + kvh * p.group + g) * kLog2e : 0.f;
-      }
+    for (int ng = 0; ng < NG; ++ng) {
+      const int g = ng * 8 + (lane & 3) * 2;
+      const float* m = p.rules.slopes ? p.rules.slopes + kvh * p.group + g : nullptr;
+      r.fall[ng] = tc::f2(m && g < p.group ? -__ldg(m) * kLog2e : 0.f, m && g + 1 < p.group ? -__ldg(m + 1) * kLog2e : 0.f);
+    }
     return r;
   } else {
     return NoRules();
@@ -400,6 +411,18 @@ __device__ __forceinline__ void consume_subtiles_f8(WarpState<D, NG>& st, uint32
     vslo[u] = rule_sees(rules, tok0 + rr, L) ? vs[rr] : 0.f;
     vshi[u] = rule_sees(rules, tok0 + rr + 8, L) ? vs[rr + 8] : 0.f;
   }
+  if constexpr (R::kOn) {
+#pragma unroll
+    for (int u = 0; u < NS; ++u)
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) {
+        sc[u][ng][0] *= kslo[u];
+        sc[u][ng][1] *= kslo[u];
+        sc[u][ng][2] *= kshi[u];
+        sc[u][ng][3] *= kshi[u];
+      }
+    rule_scores(rules, sc, sl2, tok0 + g);
+  }
   uint32_t pb[NS][NG][2];
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng) {
@@ -409,10 +432,17 @@ __device__ __forceinline__ void consume_subtiles_f8(WarpState<D, NG>& st, uint32
     for (int u = 0; u < NS; ++u) {
       const int t_lo = tok0 + u * 16 + g;
       const bool in_lo = rule_sees(rules, t_lo, L), in_hi = rule_sees(rules, t_lo + 8, L);
-      x[u][0] = in_lo ? rule_score(rules, sc[u][ng][0] * kslo[u], sl2, t_lo, ng, 0) : -INFINITY;
-      x[u][1] = in_lo ? rule_score(rules, sc[u][ng][1] * kslo[u], sl2, t_lo, ng, 1) : -INFINITY;
-      x[u][2] = in_hi ? rule_score(rules, sc[u][ng][2] * kshi[u], sl2, t_lo + 8, ng, 0) : -INFINITY;
-      x[u][3] = in_hi ? rule_score(rules, sc[u][ng][3] * kshi[u], sl2, t_lo + 8, ng, 1) : -INFINITY;
+      if constexpr (R::kOn) {
+        x[u][0] = in_lo ? sc[u][ng][0] : -INFINITY;
+        x[u][1] = in_lo ? sc[u][ng][1] : -INFINITY;
+        x[u][2] = in_hi ? sc[u][ng][2] : -INFINITY;
+        x[u][3] = in_hi ? sc[u][ng][3] : -INFINITY;
+      } else {
+        x[u][0] = in_lo ? sc[u][ng][0] * kslo[u] * sl2 : -INFINITY;
+        x[u][1] = in_lo ? sc[u][ng][1] * kslo[u] * sl2 : -INFINITY;
+        x[u][2] = in_hi ? sc[u][ng][2] * kshi[u] * sl2 : -INFINITY;
+        x[u][3] = in_hi ? sc[u][ng][3] * kshi[u] * sl2 : -INFINITY;
+      }
       mx0 = fmaxf(mx0, fmaxf(x[u][0], x[u][2]));
       mx1 = fmaxf(mx1, fmaxf(x[u][1], x[u][3]));
     }
@@ -827,7 +857,18 @@ decode_sk_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
   // [p * Wc / P, (p + 1) * Wc / P).
   const int64_t W = static_cast<int64_t>(Hkv) * CB[B];
   const int64_t Wc = static_cast<int64_t>(Hkv) * CC[B];
-  const int P = gridDim.x, pid = blockIdx.x;
+  int P = gridDim.x;
+  const int pid = blockIdx.x;
+  if constexpr (Params::kRules) {
+    // Few units: at least four tiles a CTA (fewer, and the joining of a unit's
+    // pieces costs more than the tiles), and at most 18 pieces a unit, which one
+    // CTA joins.  Measured, CTAs in all and then by this rule: 8 units of 1 to 4
+    // tiles 14.4 and 10.3 us, of 16 tiles 18.2 and 14.5, of 256 tiles 26.7 and
+    // 22.7; 2 units of 440 tiles 117 and 39; 64 units of 20 tiles alike.
+    const int units = Hkv * ((CC[B] - CB[B]) / p.seg_cost);
+    P = static_cast<int>(min(static_cast<int64_t>(P),
+                             max(static_cast<int64_t>(1), min(static_cast<int64_t>(units) * 18, max(W / 4, static_cast<int64_t>(units))))));
+  }
   auto tiles_before = [&](int64_t x) -> int64_t {  // tiles at cost positions < x
     if (x >= Wc) return W;
     int lo = 0, hi = B - 1;
@@ -840,8 +881,8 @@ decode_sk_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
     const int kvh = static_cast<int>(rel / cs), r = static_cast<int>(rel % cs);
     return static_cast<int64_t>(Hkv) * CB[lo] + static_cast<int64_t>(kvh) * nb + max(0, r - p.seg_cost);
   };
-  const int64_t t0 = tiles_before(static_cast<int64_t>(pid) * Wc / P);
-  const int64_t t1 = tiles_before(static_cast<int64_t>(pid + 1) * Wc / P);
+  const int64_t t0 = tiles_before(static_cast<int64_t>(min(pid, P)) * Wc / P);
+  const int64_t t1 = tiles_before(static_cast<int64_t>(min(pid + 1, P)) * Wc / P);
   // Fused step: the writer warps of all CTAs copy the step's new rows into
   // the caches, CTA p's warp rows p, p + P, ... (a CTA with no tiles as well)
   if (warp == kSkWriterWarp) {
@@ -1623,7 +1664,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_simt_kernel(const Para
           for (int off = 16; off > 0; off >>= 1) sdot += __shfl_xor_sync(0xffffffffu, sdot, off);
           float x = sdot * p.scale_log2;
           if constexpr (Params::kRules) {
-            if (p.rules.cap_log2 > 0.f) x = soft_cap(sdot, p.scale_log2, p.rules.cap_log2, p.rules.cap_arg);
+            if constexpr (Params::kCap) x = soft_cap(sdot, p.scale_log2, p.rules.cap_log2, p.rules.cap_arg);
             x = fmaf(-slope[g], static_cast<float>(L - 1 - (blk0 + j) * BS - o), x);
           }
           const float mn = fmaxf(mrun[g], x);
@@ -2099,15 +2140,6 @@ int check_shapes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t BS, int6
   return KV_OK;
 }
 
-// The step's new tokens for paged_decode_step (null for attention alone).
-struct StepArgs {
-  const void* k;
-  const void* v;
-  const int32_t* slot_mapping;
-  const int32_t* new_token_row;
-  int64_t num_tokens, k_stride, v_stride;  // strides in elements
-};
-
 template <typename P = DecodeParams>
 int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                 const int32_t* seq_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -2314,4 +2346,12 @@ int decode_fp8_impl(void* out, const void* q, const void* k_cache, const void* v
 }
 
 }  // namespace
+
+// The calls with score rules and a cap, compiled in a translation unit of their
+// own (both in one took twice as long as any other).
+using DecodeCall = decltype(&decode_impl<DecodeParams>);
+using DecodeFp8Call = decltype(&decode_fp8_impl<DecodeParams>);
+DecodeCall decode_rules_cap();
+DecodeFp8Call decode_rules_cap_fp8();
+
 }  // namespace pagedkv

@@ -119,6 +119,7 @@ __device__ __forceinline__ void consume_subtiles(WarpState<D, NG>& st, uint32_t 
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng) M::run(sc[u][ng], a[u], st.qf[kk][ng][0], st.qf[kk][ng][1]);
   }
+  if constexpr (R::kOn) rule_scores(rules, sc, sl2, tok0 + (lane >> 2));
   uint32_t pb[NS][NG][2];
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng) {
@@ -129,10 +130,11 @@ __device__ __forceinline__ void consume_subtiles(WarpState<D, NG>& st, uint32_t 
     for (int u = 0; u < NS; ++u) {
       const int t_lo = tok0 + u * 16 + (lane >> 2);
       const bool in_lo = rule_sees(rules, t_lo, L), in_hi = rule_sees(rules, t_lo + 8, L);
-      x[u][0] = in_lo ? rule_score(rules, sc[u][ng][0], sl2, t_lo, ng, 0) : -INFINITY;
-      x[u][1] = in_lo ? rule_score(rules, sc[u][ng][1], sl2, t_lo, ng, 1) : -INFINITY;
-      x[u][2] = in_hi ? rule_score(rules, sc[u][ng][2], sl2, t_lo + 8, ng, 0) : -INFINITY;
-      x[u][3] = in_hi ? rule_score(rules, sc[u][ng][3], sl2, t_lo + 8, ng, 1) : -INFINITY;
+      const float scl = R::kOn ? 1.f : sl2;  // scores under rules have it already
+      x[u][0] = in_lo ? sc[u][ng][0] * scl : -INFINITY;
+      x[u][1] = in_lo ? sc[u][ng][1] * scl : -INFINITY;
+      x[u][2] = in_hi ? sc[u][ng][2] * scl : -INFINITY;
+      x[u][3] = in_hi ? sc[u][ng][3] * scl : -INFINITY;
       mx0 = fmaxf(mx0, fmaxf(x[u][0], x[u][2]));
       mx1 = fmaxf(mx1, fmaxf(x[u][1], x[u][3]));
     }

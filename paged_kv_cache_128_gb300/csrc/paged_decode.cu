@@ -46,6 +46,7 @@ extern "C" int pagedkv_internal_prefill_error(int reset, int* code);
 extern "C" int pagedkv_internal_rope_error(int reset, int* code);
 extern "C" int pagedkv_internal_shared_error(int reset, int* code);
 extern "C" int pagedkv_internal_decode_rules_error(int reset, int* code);
+extern "C" int pagedkv_internal_decode_rules_cap_error(int reset, int* code);
 extern "C" int pagedkv_internal_prefill_rules_error(int reset, int* code);
 extern "C" int paged_reshape_and_cache(const void* k, const void* v, void* k_cache, void* v_cache,
                                        const int32_t* slot_mapping, int64_t num_tokens, int32_t num_kv_heads,
@@ -223,7 +224,8 @@ extern "C" int kv_device_error(int reset, int* status_out) {
   // the other translation units' words; the first that holds an error, in this order
   int (*const others[])(int, int*) = {pagedkv_internal_reshape_error, pagedkv_internal_prefill_error,
                                       pagedkv_internal_rope_error, pagedkv_internal_shared_error,
-                                      pagedkv_internal_decode_rules_error, pagedkv_internal_prefill_rules_error};
+                                      pagedkv_internal_decode_rules_error, pagedkv_internal_decode_rules_cap_error,
+                                      pagedkv_internal_prefill_rules_error};
   for (auto read : others) {
     int c = 0;
     const int r = read(reset, &c);

@@ -3,7 +3,8 @@
 // tiles start with the one that holds the first key its query sees, so a window
 // of W tokens costs what W tokens cost whatever the length, and blocks that end
 // before that key are not looked up; scores pass through the cap and the
-// distance bias before the online softmax.
+// distance bias before the online softmax.  Here without a cap; with one in
+// paged_decode_rules_cap.cu.
 
 #include "decode_kernels.cuh"
 
@@ -19,9 +20,9 @@ extern "C" int paged_decode_attention_rules(void* out, const void* q, const void
   ScoreRules rules;
   const int st = make_rules(scale, softcap, slopes, window, key_begin, nullptr, &rules);
   if (st != KV_OK) return st;
-  return decode_impl<RulesParams>(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads,
-                                  head_dim, block_size, num_blocks, max_blocks_per_seq, max_seq_len, scale, 0, dtype,
-                                  workspace, workspace_bytes, stream, nullptr, &rules);
+  return (rules.cap_log2 > 0.f ? decode_rules_cap() : &decode_impl<RulesParams<false>>)(
+      out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+      num_blocks, max_blocks_per_seq, max_seq_len, scale, 0, dtype, workspace, workspace_bytes, stream, nullptr, &rules);
 }
 
 extern "C" int paged_decode_attention_rules_fp8(
@@ -33,9 +34,10 @@ extern "C" int paged_decode_attention_rules_fp8(
   ScoreRules rules;
   const int st = make_rules(scale, softcap, slopes, window, key_begin, nullptr, &rules);
   if (st != KV_OK) return st;
-  return decode_fp8_impl<RulesParams>(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, num_seqs,
-                                      num_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
-                                      max_seq_len, scale, dtype, workspace, workspace_bytes, stream, nullptr, &rules);
+  return (rules.cap_log2 > 0.f ? decode_rules_cap_fp8() : &decode_fp8_impl<RulesParams<false>>)(
+      out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, num_seqs, num_heads, num_kv_heads, head_dim,
+      block_size, num_blocks, max_blocks_per_seq, max_seq_len, scale, dtype, workspace, workspace_bytes, stream, nullptr,
+      &rules);
 }
 
 // Read (and optionally clear) this translation unit's device error word.

@@ -95,30 +95,6 @@ struct RlSpan {
   }
 };
 
-// The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
-// P(z^2) for |z| <= 1, P of degree 5, within 6e-7 of it (the fit of soft_cap's,
-// two terms shorter: rounding the weights to 16 bits leaves 5e-4 and more).
-// With z = a dot the coefficients take the powers of a^2 and scale_log2; the
-// squares of dots it holds for end at 1 / a^2.  Where a^2 is so small that
-// a^10 would leave float32 (a cap over 3000 times the scale, which no score
-// comes near to), nothing is in range and the exact form serves.
-struct RlCap {
-  uint64_t c[6];
-  float limit;
-  __device__ __forceinline__ RlCap(float cap_arg, float scale_log2) {
-    constexpr float k[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
-                            -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
-    const float a2 = cap_arg * cap_arg;
-    float power = scale_log2;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      c[i] = tc::f2(k[i] * power, k[i] * power);
-      power *= a2;
-    }
-    limit = a2 >= 1e-7f ? 1.f / a2 : -1.f;
-  }
-};
-
 // sum += both halves of a packed pair, in float32.
 template <typename T>
 __device__ __forceinline__ void add_pair(float& sum, uint32_t w) {
@@ -526,7 +502,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     const float* const row_other = row_own + (half ? -kTcRows : kTcRows);
     const float c2 = p.scale_log2;
     const uint64_t c2x2 = tc::f2(c2, c2);
-    const RlCap cap(p.rules.cap_arg, c2);
+    const CapPoly cap(p.rules.cap_arg, c2);
     // a tile whose weights sum to more than this has moved too far above its row's reference
     constexpr float kGrown = kBf16 ? 1.0995116e12f : 16384.f;  // 2^40: fp32 sums; 2^14: fp16 weights
     bool ok = true;
@@ -578,7 +554,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         auto row_max = [&]() {
           float m = -INFINITY;
           auto scan = [&](auto in_full) -> bool {
-            constexpr bool kExact = decltype(in_full)::value;
+            [[maybe_unused]] constexpr bool kExact = decltype(in_full)::value;
             float big = 0.f;
             m = -INFINITY;
 #pragma unroll 1
@@ -657,13 +633,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                   x.x = in0 ? x.x : 0.f;
                   x.y = in1 ? x.y : 0.f;
                 }
-                const uint64_t d = tc::f2(x.x, x.y), u = tc::fmul2(d, d);
-                const float2 u2 = tc::f2_split(u);
-                big = max3(big, u2.x, u2.y);
-                uint64_t y = tc::ffma2(cap.c[5], u, cap.c[4]);
-#pragma unroll
-                for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, cap.c[j]);
-                e = tc::f2_split(tc::ffma2(d, y, base));
+                e = tc::f2_split(cap.run(tc::f2(x.x, x.y), base, big));
               } else {
                 e = tc::f2_split(tc::ffma2(tc::f2(x.x, x.y), c2x2, base));
               }

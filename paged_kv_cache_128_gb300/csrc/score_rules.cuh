@@ -10,8 +10,10 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace pagedkv {
 
@@ -83,34 +85,113 @@ __device__ __forceinline__ float soft_cap(float dot, float scale_log2, float cap
   return copysignf(fmaf(-2.f * cap_log2, inv, cap_log2), z);  // NaN: copysign keeps it
 }
 
+// The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
+// P(z^2) for |z| <= 1, P of degree 5, within 6e-7 of it (the fit of soft_cap's,
+// two terms shorter: rounding the weights to 16 bits leaves 5e-4 and more).
+// With z = a dot the coefficients take the powers of a^2 and scale_log2; the
+// squares of dots it holds for end at 1 / a^2.  Where a^2 is so small that
+// a^10 would leave float32 (a cap over 3000 times the scale, which no score
+// comes near to), nothing is in range and the exact form serves.
+struct CapPoly {
+  uint64_t c[6];
+  float limit;
+  __device__ __forceinline__ CapPoly(float cap_arg, float scale_log2) {
+    constexpr float k[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
+                            -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
+    const float a2 = cap_arg * cap_arg;
+    float power = scale_log2;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      c[i] = tc::f2(k[i] * power, k[i] * power);
+      power *= a2;
+    }
+    limit = a2 >= 1e-7f ? 1.f / a2 : -1.f;
+  }
+  // base + the capped scores of two dots; `big` collects the largest square,
+  // which the caller compares with limit.
+  __device__ __forceinline__ uint64_t run(uint64_t dots, uint64_t base, float& big) const {
+    const uint64_t u = tc::fmul2(dots, dots);
+    const float2 u2 = tc::f2_split(u);
+    big = max3(big, u2.x, u2.y);
+    uint64_t y = tc::ffma2(c[5], u, c[4]);
+#pragma unroll
+    for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, c[j]);
+    return tc::ffma2(dots, y, base);
+  }
+};
+
+// soft_cap out of line, for the rare scores beyond the cap.
+static __device__ __noinline__ float soft_cap_far(float dot, float scale_log2, float cap_log2, float cap_arg) {
+  return soft_cap(dot, scale_log2, cap_log2, cap_arg);
+}
+
 // The rules of one decode tile for one lane of its warp (heads ng * 8 +
 // (lane % 4) * 2 + c), and their absence.
 struct NoRules {
   static constexpr bool kOn = false;
 };
-template <int NG>
+template <int NG, bool CAP>
 struct TileRules {
-  static constexpr bool kOn = true;
+  static constexpr bool kOn = true, kCap = CAP;
   float cap_log2, cap_arg;
-  float slope[NG][2];  // slope * log2(e)
-  int lo;              // first key seen
-  int pos;             // the query's position
+  uint64_t fall[NG];  // -slope * log2(e) of the lane's two heads
+  int lo;             // first key seen
+  int pos;            // the query's position
 };
 
-// A key's score in the exp2 domain from its dot product.
-template <typename R>
-__device__ __forceinline__ float rule_score(const R& r, float dot, float scale_log2, int t, int ng, int c) {
-  if constexpr (!R::kOn) {
-    return dot * scale_log2;
-  } else {
-    const float x = r.cap_log2 > 0.f ? soft_cap(dot, scale_log2, r.cap_log2, r.cap_arg) : dot * scale_log2;
-    return fmaf(-r.slope[ng][c], static_cast<float>(r.pos - t), x);
-  }
-}
 template <typename R>
 __device__ __forceinline__ bool rule_sees(const R& r, int t, int L) {
   if constexpr (R::kOn) return t >= r.lo && t < L;
   else return t < L;
+}
+
+// The dots of NS 16-token sub-tiles (tokens t0 + 16 u and + 8 further, two
+// heads each) into scores under the rules, in the exp2 domain.
+template <int NS, int NG, bool CAP>
+__device__ __forceinline__ void rule_scores(const TileRules<NG, CAP>& r, float (&sc)[NS][NG][4], float scale_log2,
+                                            int t0) {
+  const CapPoly cap(r.cap_arg, scale_log2);
+  const uint64_t sl2 = tc::f2(scale_log2, scale_log2);
+  if constexpr (CAP) {
+    // Scores beyond the cap (or in slots that are not seen, at a cost in time
+    // only): the exact form, out of line.
+    float far = 0.f;
+#pragma unroll
+    for (int u = 0; u < NS; ++u)
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) far = max3(far, fabsf(sc[u][ng][e]), fabsf(sc[u][ng][e + 1]));
+    if (__any_sync(0xffffffffu, far * far > cap.limit)) {
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float away = static_cast<float>(r.pos - t0 - u * 16 - (e >> 1) * 8);
+            const float2 fall = tc::f2_split(r.fall[ng]);
+            sc[u][ng][e] = fmaf(e & 1 ? fall.y : fall.x, away,
+                                soft_cap_far(sc[u][ng][e], scale_log2, r.cap_log2, r.cap_arg));
+          }
+      return;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < NS; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float away = static_cast<float>(r.pos - t0 - u * 16 - h * 8);
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) {
+        float* d = &sc[u][ng][2 * h];
+        const uint64_t bias = tc::fmul2(r.fall[ng], tc::f2(away, away)), x = tc::f2(d[0], d[1]);
+        float unused = 0.f;
+        const float2 y = tc::f2_split(CAP ? cap.run(x, bias, unused) : tc::ffma2(x, sl2, bias));
+        d[0] = y.x;
+        d[1] = y.y;
+      }
+    }
 }
 
 }  // namespace pagedkv

@@ -135,9 +135,11 @@ def test_slopes_of_either_sign_over_a_long_cache(sign):
 def test_no_rules_is_the_plain_call():
     t = PagedBatch("bf16", 28, 4, 128, 16, [700, 64, 1, 0, 999], seed=2)
     _run(t)
+    t.check()
+    # (not to the bit: few units are cut into fewer pieces, whose float32 sums are joined in another order)
     plain = torch.empty_like(t.out)
     pk.paged_decode_attention(plain, t.q, t.kc, t.vc, t.tables, t.seq_lens, t.scale, 999)
-    assert torch.equal(plain, t.out)
+    t.check(out=plain)
 
 
 def test_more_sequences_than_the_stream_kernel_takes():
