@@ -62,6 +62,10 @@ template <typename T, bool F8> struct RopeShape {
 
 constexpr int kRopeAxes = 4, kRopeAxisPairs = 256;
 
+// One position a token; several, with the pairs in runs of eight (a lane's
+// share) of one axis; several in any order.
+enum RopeAxes { kOneAxis = 0, kAxisRuns = 1, kAnyAxis = 2 };
+
 struct RopeParams {
   void* q_out;
   const void* q;
@@ -80,7 +84,7 @@ struct RopeParams {
   // several axes (num_axes > 1): positions [num_axes][num_tokens], and the axis
   // of each pair, two bits each from the lowest on
   int64_t num_tokens;
-  int32_t num_axes;
+  int32_t num_axes, axis_runs;  // axis_runs: pairs 8 i .. 8 i + 7 are of one axis
   uint64_t axis_of_pair[kRopeAxisPairs / 32];
 };
 
@@ -162,7 +166,7 @@ __device__ __forceinline__ void rotate16(float (&x0)[8], float (&x1)[8], const f
 // One CTA per (token, part): the part's rounds of heads.  F8: K and V are
 // quantised, a head's D / 16 lanes (4, 8 or 16, so within one warp) taking
 // the row's largest magnitude by shuffles.
-template <typename T, bool INTER, bool F8, bool AXES>
+template <typename T, bool INTER, bool F8, RopeAxes AXES>
 __global__ void __launch_bounds__(kRopeThreads, (RopeShape<T, F8>::kCtas))
 rope_cache_kernel(const RopeParams p, int threads) {
   constexpr int kUnits = RopeShape<T, F8>::kUnits;
@@ -182,8 +186,8 @@ rope_cache_kernel(const RopeParams p, int threads) {
   const int32_t slot = __ldg(p.slot_mapping + t);
   int32_t pos[kRopeAxes];
 #pragma unroll
-  for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a)
-    if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES ? a * p.num_tokens : 0) + t);
+  for (int a = 0; a < (AXES != kOneAxis ? kRopeAxes : 1); ++a)
+    if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES != kOneAxis ? a * p.num_tokens : 0) + t);
   Run8<T> r[kUnits][2];
   auto load = [&](int h0) {
 #pragma unroll
@@ -203,14 +207,16 @@ rope_cache_kernel(const RopeParams p, int threads) {
   // out beside those (a padded token's rows are read and dropped)
   load(first);
   const bool reporter = tid == 0 && blockIdx.y == 0;
-  if (AXES ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) return;
-  // With several axes the CTA first gathers the token's own row of angles, a
-  // thread per pair from its axis' row of the table (each lane picking its
-  // pairs from up to four rows took 40 registers into spills: 43.0 us instead
-  // of 32.8 for 8192 tokens of 28 + 2 x 4 heads of 128).
+  if (AXES != kOneAxis ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) return;
+  // With axes in any order the CTA first gathers the token's own row of angles,
+  // a thread per pair from its axis' row of the table (each lane picking its
+  // pairs from up to four rows took 40 registers into spills: 43.0 us instead of
+  // 33.1 for 8192 tokens of 28 + 2 x 4 heads of 128).  Where a lane's eight pairs
+  // are of one axis it reads them from that axis' row (31.1 us; with one position
+  // a token 29.4).
   const float* row;
-  __shared__ __align__(16) float own_row[AXES ? 2 * kRopeAxisPairs : 4];
-  if constexpr (AXES) {
+  __shared__ __align__(16) float own_row[AXES == kAnyAxis ? 2 * kRopeAxisPairs : 4];
+  if constexpr (AXES == kAnyAxis) {
     for (int i = tid; i < half; i += threads) {
       const float* from = p.cos_sin + rope_position(p, pos, i) * static_cast<int64_t>(p.rot_dim) + i;
       own_row[i] = __ldg(from);
@@ -219,14 +225,15 @@ rope_cache_kernel(const RopeParams p, int threads) {
     __syncthreads();
     row = own_row + col * 8;
   } else {
-    row = p.cos_sin + static_cast<int64_t>(pos[0]) * p.rot_dim + col * 8;
+    const int32_t at = AXES == kOneAxis || !turn ? pos[0] : rope_position(p, pos, col * 8);
+    row = p.cos_sin + static_cast<int64_t>(at) * p.rot_dim + col * 8;
   }
   float c[8], s[8];
   if (turn) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       float4 cv, sv;
-      if constexpr (AXES) {
+      if constexpr (AXES == kAnyAxis) {
         cv = *reinterpret_cast<const float4*>(row + i);
         sv = *reinterpret_cast<const float4*>(row + half + i);
       } else {
@@ -308,7 +315,7 @@ rope_cache_kernel(const RopeParams p, int threads) {
 // Any head_dim, any even rot_dim, any alignment of the elements: one warp
 // per (token, head), lanes over the pairs and then over the values that pass
 // through.  F8 walks a K or V row twice (its largest magnitude, its codes).
-template <typename T, bool INTER, bool F8, bool AXES>
+template <typename T, bool INTER, bool F8, RopeAxes AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_cache_any_kernel(const RopeParams p, int64_t num_tokens) {
   const int lane = threadIdx.x & 31;
   const int heads = p.num_heads + 2 * p.num_kv_heads, D = p.head_dim, half = p.rot_dim >> 1;
@@ -319,17 +326,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cache_any_kernel(const Rope
     const int32_t slot = __ldg(p.slot_mapping + t);
     int32_t pos[kRopeAxes];
 #pragma unroll
-    for (int a = 0; a < (AXES ? kRopeAxes : 1); ++a)
-      if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES ? a * p.num_tokens : 0) + t);
+    for (int a = 0; a < (AXES != kOneAxis ? kRopeAxes : 1); ++a)
+      if (a == 0 || a < p.num_axes) pos[a] = __ldg(p.positions + (AXES != kOneAxis ? a * p.num_tokens : 0) + t);
     const bool reporter = lane == 0 && h == 0;
-    if (AXES ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) continue;
+    if (AXES != kOneAxis ? !rope_token_axes(p, pos, slot, reporter) : !rope_token(p, pos[0], slot, reporter)) continue;
     const bool is_q = h < p.num_heads, is_v = h >= p.num_heads + p.num_kv_heads;
     const int hk = h - p.num_heads - (is_v ? p.num_kv_heads : 0);
     const T* src = is_q ? static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * D
                         : static_cast<const T*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) +
                               static_cast<int64_t>(hk) * D;
     auto row_of = [&](int i) {  // the table row of pair i
-      return p.cos_sin + static_cast<int64_t>(AXES ? rope_position(p, pos, i) : pos[0]) * p.rot_dim;
+      return p.cos_sin + static_cast<int64_t>(AXES != kOneAxis ? rope_position(p, pos, i) : pos[0]) * p.rot_dim;
     };
     const int turned = is_v ? 0 : p.rot_dim;
     // visit(e, y): every output value of the row once, pairs first
@@ -373,13 +380,13 @@ int rope_sms() {
   return sms > 0 ? sms : 1;
 }
 
-template <typename T, bool INTER, bool F8, bool AXES>
+template <typename T, bool INTER, bool F8, RopeAxes AXES>
 cudaError_t launch_rope(const RopeParams& p, int64_t n, bool vec, cudaStream_t st) {
   const int heads = p.num_heads + 2 * p.num_kv_heads;
   const int64_t sms = rope_sms();
   if (!vec) {
     const int64_t need = (n * heads + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    rope_cache_any_kernel<T, INTER, F8, AXES>
+    rope_cache_any_kernel<T, INTER, F8, AXES == kAxisRuns ? kAnyAxis : AXES>
         <<<static_cast<unsigned>(need < sms * 64 ? need : sms * 64), kRopeThreads, 0, st>>>(p, n);
     return cudaGetLastError();
   }
@@ -396,9 +403,14 @@ cudaError_t launch_rope(const RopeParams& p, int64_t n, bool vec, cudaStream_t s
 template <typename T, bool F8>
 cudaError_t launch_rope_form(const RopeParams& p, int64_t n, bool vec, bool inter, cudaStream_t st) {
   // one axis: the single-position kernels, its row of positions being the only one
-  if (p.num_axes > 1)
-    return inter ? launch_rope<T, true, F8, true>(p, n, vec, st) : launch_rope<T, false, F8, true>(p, n, vec, st);
-  return inter ? launch_rope<T, true, F8, false>(p, n, vec, st) : launch_rope<T, false, F8, false>(p, n, vec, st);
+  if (p.num_axes <= 1)
+    return inter ? launch_rope<T, true, F8, kOneAxis>(p, n, vec, st)
+                 : launch_rope<T, false, F8, kOneAxis>(p, n, vec, st);
+  if (p.axis_runs)
+    return inter ? launch_rope<T, true, F8, kAxisRuns>(p, n, vec, st)
+                 : launch_rope<T, false, F8, kAxisRuns>(p, n, vec, st);
+  return inter ? launch_rope<T, true, F8, kAnyAxis>(p, n, vec, st)
+               : launch_rope<T, false, F8, kAnyAxis>(p, n, vec, st);
 }
 
 // Checks shared by the entry points, then the launch.
@@ -469,8 +481,10 @@ int rope_axes(RopeParams& p, int64_t num_tokens, int32_t num_axes, const uint8_t
   if (p.rot_dim <= 0 || p.rot_dim % 2 != 0 || p.rot_dim / 2 > kRopeAxisPairs || !pair_axes) return KV_ERR_INVALID_ARG;
   p.num_tokens = num_tokens;
   p.num_axes = num_axes;
+  p.axis_runs = 1;
   for (int i = 0; i < p.rot_dim / 2; ++i) {
     if (pair_axes[i] >= num_axes) return KV_ERR_INVALID_ARG;
+    if (pair_axes[i] != pair_axes[i & ~7]) p.axis_runs = 0;
     p.axis_of_pair[i >> 5] |= static_cast<uint64_t>(pair_axes[i]) << (2 * (i & 31));
   }
   return KV_OK;
