@@ -142,6 +142,7 @@ __device__ __forceinline__ auto tile_rules(const P& p, int kvh, int L, int lo, i
     TileRules<NG, P::kCap> r;
     r.cap_log2 = p.rules.cap_log2;
     r.cap_arg = p.rules.cap_arg;
+    r.poly = p.rules.poly;
     r.lo = lo;
     r.pos = L - 1;
 #pragma unroll

@@ -502,9 +502,9 @@ __global__ void __launch_bounds__(kRlThreads, 1)
     const float* const row_other = row_own + (half ? -kTcRows : kTcRows);
     const float c2 = p.scale_log2;
     const uint64_t c2x2 = tc::f2(c2, c2);
-    const CapPoly cap(p.rules.cap_arg, c2);
+    const CapPoly cap = p.rules.poly;
     // a tile whose weights sum to more than this has moved too far above its row's reference
-    constexpr float kGrown = kBf16 ? 1.0995116e12f : 16384.f;  // 2^40: fp32 sums; 2^14: fp16 weights
+    constexpr float kGrown = kBf16 ? 4294967296.f : 16384.f;  // 2^32: P V stays in float32; 2^14: P in fp16
     bool ok = true;
     int scores = 0;  // S tiles so far
     for (int k = 0;; ++k) {
@@ -573,9 +573,9 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                   } else {
                     const float u = d * d;
                     big = fmaxf(big, u);
-                    float y = fmaf(tc::f2_split(cap.c[5]).x, u, tc::f2_split(cap.c[4]).x);
+                    float y = fmaf(cap.c[5].x, u, cap.c[4].x);
 #pragma unroll
-                    for (int j = 3; j >= 0; --j) y = fmaf(y, u, tc::f2_split(cap.c[j]).x);
+                    for (int j = 3; j >= 0; --j) y = fmaf(y, u, cap.c[j].x);
                     x = d * y;
                   }
                 }

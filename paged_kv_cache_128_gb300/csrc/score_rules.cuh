@@ -19,6 +19,27 @@ namespace pagedkv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
+// P(z^2) for |z| <= 1, P of degree 5, within 6e-7 of it (the fit of soft_cap's,
+// two terms shorter: rounding the weights to 16 bits leaves 5e-4 and more).
+// With z = a dot the coefficients take the powers of a^2 and scale_log2; the
+// squares of dots it holds for end at 1 / a^2.  They are made on the host.
+struct CapPoly {
+  float2 c[6];  // each coefficient twice
+  float limit;
+  // base + the capped scores of two dots; `big` collects the largest square,
+  // which the caller compares with limit.
+  __device__ __forceinline__ uint64_t run(uint64_t dots, uint64_t base, float& big) const {
+    const uint64_t u = tc::fmul2(dots, dots);
+    const float2 u2 = tc::f2_split(u);
+    big = max3(big, u2.x, u2.y);
+    uint64_t y = tc::ffma2(tc::f2(c[5].x, c[5].y), u, tc::f2(c[4].x, c[4].y));
+#pragma unroll
+    for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, tc::f2(c[j].x, c[j].y));
+    return tc::ffma2(dots, y, base);
+  }
+};
+
 struct ScoreRules {
   float cap_log2;            // cap * log2(e); 0: no cap
   float cap_arg;             // scale / cap: dot * cap_arg is tanh's argument
@@ -26,6 +47,7 @@ struct ScoreRules {
   const int32_t* key_begin;  // [query rows] first key seen, or null
   const int32_t* key_end;    // [query rows] one past the last key seen, or null (prefill only)
   int32_t window;            // keys seen up to and with the query's own; 0: all
+  CapPoly poly;              // the cap's polynomial
 };
 
 // The rules of a call, checked.
@@ -35,12 +57,25 @@ inline int make_rules(float scale, float softcap, const float* slopes, int32_t w
   const uintptr_t bits = reinterpret_cast<uintptr_t>(slopes) | reinterpret_cast<uintptr_t>(key_begin) |
                          reinterpret_cast<uintptr_t>(key_end);
   if (bits % 4 != 0) return KV_ERR_INVALID_ARG;
-  ScoreRules r{0.f, 0.f, slopes, key_begin, key_end, window};
+  ScoreRules r{0.f, 0.f, slopes, key_begin, key_end, window, {}};
   if (softcap > 0.f) {
     r.cap_log2 = softcap * kLog2e;
     r.cap_arg = scale / softcap;
     // a cap so large or small that these leave float32
     if (!std::isfinite(r.cap_log2) || !(r.cap_log2 > 0.f) || !std::isfinite(r.cap_arg)) return KV_ERR_INVALID_ARG;
+    constexpr float k[6] = {0.9999994039535522f,    -0.3332904279232025f,  0.13281433284282684f,
+                            -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
+    // Where a^2 is so small that a^10 would leave float32 (a cap over 3000 times
+    // the scale, which scores hardly come near to) nothing is in range and the
+    // exact form serves.
+    const double a2 = static_cast<double>(r.cap_arg) * r.cap_arg;
+    const bool fits = a2 >= 1e-7 && a2 <= 1e7;
+    double power = static_cast<double>(scale) * kLog2e;
+    for (int i = 0; i < 6; ++i) {
+      r.poly.c[i].x = r.poly.c[i].y = fits ? static_cast<float>(k[i] * power) : 0.f;
+      power *= a2;
+    }
+    r.poly.limit = fits ? static_cast<float>(1.0 / a2) : -1.f;
   }
   *out = r;
   return KV_OK;
@@ -85,41 +120,6 @@ __device__ __forceinline__ float soft_cap(float dot, float scale_log2, float cap
   return copysignf(fmaf(-2.f * cap_log2, inv, cap_log2), z);  // NaN: copysign keeps it
 }
 
-// The cap for packed pairs, as a polynomial in the dot product: tanh(z) = z
-// P(z^2) for |z| <= 1, P of degree 5, within 6e-7 of it (the fit of soft_cap's,
-// two terms shorter: rounding the weights to 16 bits leaves 5e-4 and more).
-// With z = a dot the coefficients take the powers of a^2 and scale_log2; the
-// squares of dots it holds for end at 1 / a^2.  Where a^2 is so small that
-// a^10 would leave float32 (a cap over 3000 times the scale, which no score
-// comes near to), nothing is in range and the exact form serves.
-struct CapPoly {
-  uint64_t c[6];
-  float limit;
-  __device__ __forceinline__ CapPoly(float cap_arg, float scale_log2) {
-    constexpr float k[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281433284282684f,
-                            -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
-    const float a2 = cap_arg * cap_arg;
-    float power = scale_log2;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      c[i] = tc::f2(k[i] * power, k[i] * power);
-      power *= a2;
-    }
-    limit = a2 >= 1e-7f ? 1.f / a2 : -1.f;
-  }
-  // base + the capped scores of two dots; `big` collects the largest square,
-  // which the caller compares with limit.
-  __device__ __forceinline__ uint64_t run(uint64_t dots, uint64_t base, float& big) const {
-    const uint64_t u = tc::fmul2(dots, dots);
-    const float2 u2 = tc::f2_split(u);
-    big = max3(big, u2.x, u2.y);
-    uint64_t y = tc::ffma2(c[5], u, c[4]);
-#pragma unroll
-    for (int j = 3; j >= 0; --j) y = tc::ffma2(y, u, c[j]);
-    return tc::ffma2(dots, y, base);
-  }
-};
-
 // soft_cap out of line, for the rare scores beyond the cap.
 static __device__ __noinline__ float soft_cap_far(float dot, float scale_log2, float cap_log2, float cap_arg) {
   return soft_cap(dot, scale_log2, cap_log2, cap_arg);
@@ -134,6 +134,7 @@ template <int NG, bool CAP>
 struct TileRules {
   static constexpr bool kOn = true, kCap = CAP;
   float cap_log2, cap_arg;
+  CapPoly poly;
   uint64_t fall[NG];  // -slope * log2(e) of the lane's two heads
   int lo;             // first key seen
   int pos;            // the query's position
@@ -150,7 +151,7 @@ __device__ __forceinline__ bool rule_sees(const R& r, int t, int L) {
 template <int NS, int NG, bool CAP>
 __device__ __forceinline__ void rule_scores(const TileRules<NG, CAP>& r, float (&sc)[NS][NG][4], float scale_log2,
                                             int t0) {
-  const CapPoly cap(r.cap_arg, scale_log2);
+  const CapPoly& cap = r.poly;
   const uint64_t sl2 = tc::f2(scale_log2, scale_log2);
   if constexpr (CAP) {
     // Scores beyond the cap (or in slots that are not seen, at a cost in time
