@@ -515,24 +515,37 @@ int paged_prefill_attention(void* out, const void* q, const void* k_cache, const
  * A key that a query does not see takes no part in its row, whatever K holds
  * there, and blocks that end before the first key seen are not looked up:
  * their table entries may be anything, as when a window's old blocks have been
- * released.  tanh is accurate to float32 (a polynomial for |s| <= c,
- * exponentials beyond).
+ * released.  The cap is within 7e-7 of the score (2e-7 in float32 calls).
  *
  * paged_prefill_attention with rules: key_begin and key_end have one entry per
  * row of q (positions in the row's sequence), so that a row can see its whole
  * image or prefix (key_end past its own position) or only its document.
  * Values: a row's weight on a key it does not see is 0, and V there is cleared
- * where no row of a tile (128 / heads consecutive tokens; 64 in the mma.sync
+ * where no row of a tile (256 / heads consecutive tokens, heads the largest
+ * power of two up to 8 that divides num_heads / num_kv_heads; 64 in the mma.sync
  * kernel) sees it; a NaN or infinity in the value of a key that another row of
- * the tile sees can reach the row.  Other arguments and rules are those of
- * paged_prefill_attention. */
+ * the tile sees can reach the row.
+ *   workspace: where few rows see many keys, the keys are cut into pieces that
+ *     several CTAs take, joined in order; their parts lie here, device memory of
+ *     paged_prefill_rules_workspace_size bytes, 16-byte aligned, whose contents
+ *     need not be kept.  NULL: the keys are not cut.
+ * Other arguments and rules are those of paged_prefill_attention. */
 int paged_prefill_attention_rules(void* out, const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* block_tables, const int32_t* seq_lens,
                                   const int32_t* query_start_loc, int64_t num_query_tokens, int32_t num_seqs,
                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                   int64_t num_blocks, int32_t max_blocks_per_seq, int32_t max_query_len, float scale,
                                   float softcap, const float* slopes, int32_t window, const int32_t* key_begin,
-                                  const int32_t* key_end, int dtype, void* stream);
+                                  const int32_t* key_end, int dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Workspace bytes of paged_prefill_attention_rules for these arguments (no
+ * passage, as there; 0: it needs none).  intervals: whether the call gives
+ * key_begin or key_end. */
+int paged_prefill_rules_workspace_size(int64_t num_query_tokens, int32_t num_seqs, int32_t num_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                       int32_t max_blocks_per_seq, int32_t max_query_len, int32_t window,
+                                       int32_t intervals, size_t* bytes_out);
 
 /* paged_decode_attention with the score rules above (no passage, as there):
  * the query is at position i = seq_lens[b] - 1, key_begin has one entry per

@@ -31,6 +31,7 @@ def __getattr__(name):
                 "paged_decode_attention_fp8", "paged_decode_step_fp8", "paged_prefill_attention",
                 "rope_and_cache", "rope_and_cache_fp8", "paged_decode_attention_shared_prefix",
                 "rope_and_cache_axes", "rope_and_cache_axes_fp8", "paged_prefill_attention_rules",
+                "prefill_rules_workspace",
                 "paged_decode_attention_rules", "paged_decode_attention_rules_fp8",
                 "shared_prefix_workspace"):
         from . import kernels

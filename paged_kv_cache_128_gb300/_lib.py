@@ -102,7 +102,9 @@ SIGNATURES = {
     "paged_prefill_attention_rules": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_int64, c_int32, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32,
                                               c_int32, c_float, c_float, c_void_p, c_int32, c_void_p, c_void_p, c_int,
-                                              c_void_p]),
+                                              c_void_p, c_size_t, c_void_p]),
+    "paged_prefill_rules_workspace_size": (c_int, [c_int64, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                   c_int32, c_int32, c_int32, POINTER(c_size_t)]),
     "paged_decode_attention_rules": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
                                              c_int32, c_int32, c_int32, c_int32, c_int64, c_int32, c_int64, c_float,
                                              c_float, c_void_p, c_int32, c_void_p, c_int, c_void_p, c_size_t,

@@ -74,7 +74,8 @@ struct RlItem {
   int ctx, len;     // positions before the chunk, and in all
   int tok0, head0;  // first chunk token of the pair, first head of the group
   int key_lo, key_hi;          // keys that some row of the pair sees
-  int tile_lo[2], tile_hi[2];  // key tiles of each query tile (none: equal)
+  int piece, first, end;       // the piece of them that this is, its tiles first down to end (none: first < end)
+  int tile_lo[2], tile_hi[2];  // key tiles of each query tile in the piece (none: equal)
   int tile0;                   // tiles before the item's first
 };
 
@@ -83,8 +84,8 @@ struct RlItem {
 struct RlSpan {
   int first, end, own_lo, own_hi, other_lo, other_hi, tile0;
   __device__ __forceinline__ RlSpan(const RlItem& it, int q)
-      : first((it.key_hi + kTcKeys - 1) / kTcKeys - 1), end(it.key_lo / kTcKeys), own_lo(it.tile_lo[q]),
-        own_hi(it.tile_hi[q]), other_lo(it.tile_lo[q ^ 1]), other_hi(it.tile_hi[q ^ 1]), tile0(it.tile0) {}
+      : first(it.first), end(it.end), own_lo(it.tile_lo[q]), own_hi(it.tile_hi[q]), other_lo(it.tile_lo[q ^ 1]),
+        other_hi(it.tile_hi[q ^ 1]), tile0(it.tile0) {}
   __device__ __forceinline__ bool own(int kt) const { return kt >= own_lo && kt < own_hi; }
   __device__ __forceinline__ bool other(int kt) const { return kt >= other_lo && kt < other_hi; }
   __device__ __forceinline__ bool any(int kt) const { return own(kt) || other(kt); }
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // grid, ..., every other round in reverse, so that the sums even out.
       // Sequences are looked at 32 at a time, a lane each, and once: what has
       // no rows has no items, whatever max_query_len allows for.
+      const int64_t per_pair = static_cast<int64_t>(ngroups) * p.splits;
       int64_t round = 0, before = 0;  // items of the sequences before this chunk of 32
       auto item_of = [&](int64_t r) {
         return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           if (bad || my_len < my_n) my_n = 0;
         }
         const int my_pairs = min(max(my_n, 0) / (2 * tpt) + (max(my_n, 0) % (2 * tpt) != 0), p.row_tiles);
-        int64_t upto = static_cast<int64_t>(my_pairs) * ngroups;  // items up to and with this lane's sequence
+        int64_t upto = static_cast<int64_t>(my_pairs) * per_pair;  // items up to and with this lane's sequence
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
@@ -306,11 +308,12 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           const int64_t x = item_of(round);
           const int src = __ffs(__ballot_sync(0xffffffffu, x < upto)) - 1;  // the lane whose sequence x lies in
           const int pairs = __shfl_sync(0xffffffffu, my_pairs, src);
-          const int64_t rel = x - (__shfl_sync(0xffffffffu, upto, src) - static_cast<int64_t>(pairs) * ngroups);
-          const int b = b0 + src, gi = static_cast<int>(rel % ngroups);
-          const int pair = pairs - 1 - static_cast<int>(rel / ngroups);
+          const int64_t rel = x - (__shfl_sync(0xffffffffu, upto, src) - static_cast<int64_t>(pairs) * per_pair);
+          const int b = b0 + src, gi = static_cast<int>(rel % per_pair / p.splits);
+          const int pair = pairs - 1 - static_cast<int>(rel / per_pair);
           RlItem it;
           it.seq = b;
+          it.piece = static_cast<int>(rel % p.splits);
           it.q_row = __shfl_sync(0xffffffffu, my_row, src);
           it.n = __shfl_sync(0xffffffffu, my_n, src);
           it.len = __shfl_sync(0xffffffffu, my_len, src);
@@ -344,9 +347,31 @@ __global__ void __launch_bounds__(kRlThreads, 1)
               it.key_hi = max(it.key_hi, hi);
             }
           }
+          // The piece: an equal share of the tiles, of which each query tile has
+          // what it needs; first and end are tiles that one of them needs.
+          it.first = -1;
+          it.end = 0;
+          if (it.key_lo < it.key_hi) {
+            const int lowest = it.key_lo / kTcKeys, tiles = (it.key_hi + kTcKeys - 1) / kTcKeys - lowest;
+            const int from = lowest + static_cast<int>(static_cast<int64_t>(tiles) * it.piece / p.splits);
+            const int to = lowest + static_cast<int>(static_cast<int64_t>(tiles) * (it.piece + 1) / p.splits);
+            int end = INT32_MAX;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              it.tile_lo[q] = max(it.tile_lo[q], from);
+              it.tile_hi[q] = min(it.tile_hi[q], to);
+              if (it.tile_lo[q] < it.tile_hi[q]) {
+                end = min(end, it.tile_lo[q]);
+                it.first = max(it.first, it.tile_hi[q] - 1);
+              } else {
+                it.tile_lo[q] = it.tile_hi[q] = 0;
+              }
+            }
+            if (it.first >= 0) it.end = end;
+          }
           it.tile0 = loaded;
           hand_on(it);
-          if (!ok || it.key_lo >= it.key_hi) continue;
+          if (!ok || it.first < it.end) continue;
           const int kvh = it.head0 / p.group;
           const RlSpan walk(it, 0);
           int kt = walk.below(walk.first + 1);
@@ -518,6 +543,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       const int pos = items[slot].ctx + t, head = items[slot].head0 + hh, len = items[slot].len;
       const int key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
       const int64_t row = static_cast<int64_t>(items[slot].q_row) + t;
+      const int piece = items[slot].piece;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_free + slot);
       if (last) break;
@@ -721,8 +747,11 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         if (lane == 0) mbar_arrive(bar_p + q);
       }
       T* orow = static_cast<T*>(p.out) + (row * p.num_heads + head) * D + half * (D / 2);
+      const int64_t part = static_cast<int64_t>(piece) * p.num_tokens * p.num_heads + row * p.num_heads + head;
       if (!begun) {  // the tile sees no key
-        if (real)
+        if (real && p.splits > 1) {
+          if (half == 0) *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(-INFINITY, 0.f);
+        } else if (real)
           for (int oc = 0; oc < D / 2; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
         continue;
       }
@@ -733,16 +762,29 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       if (ok && !rl_wait(bar_pv + q, (scores - 1) & 1)) ok = false;
       tc::fence_after();
       const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
+      const bool store = ok && real;
+      if (p.splits > 1 && store && half == 0)
+        *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(l == 0.f ? -INFINITY : m_ref, l);
 #pragma unroll 1
       for (int oc = 0; oc < D / 2; oc += 32) {
         uint32_t w[32];
         tc::ld_32x32b_x32(tO + oc, w);
         tc::wait_ld();
+        if (p.splits > 1) {  // joined by join_pieces_kernel
+          if (store) {
+            float4* to = reinterpret_cast<float4*>(p.ws_o + part * D + half * (D / 2) + oc);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              to[j] = make_float4(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1]),
+                                  __uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3]));
+          }
+          continue;
+        }
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           o[j] = Mma<T>::pack(__uint_as_float(w[2 * j]) * inv, __uint_as_float(w[2 * j + 1]) * inv);
-        if (ok && real) {
+        if (store) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             reinterpret_cast<uint4*>(orow + oc)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
@@ -762,32 +804,123 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   }
 }
 
+// Joins the pieces of a row, a warp per (row, head): M = max_s m_s, out =
+// sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, in the order of the pieces.
+// Rows that no sequence's chunk has, or past what was computed, are left.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) join_pieces_kernel(const RulesPrefillParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = p.num_tokens * p.num_heads;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (idx >= rows) return;
+  const int64_t row = idx / p.num_heads;
+  // the last sequence that starts at or before the row, among those with rows
+  int lo = 0, hi = p.num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(p.query_start + mid) <= row) lo = mid; else hi = mid - 1;
+  }
+  const int q_row = __ldg(p.query_start + lo), n = __ldg(p.query_start + lo + 1) - q_row;
+  int len = __ldg(p.seq_lens + lo);
+  const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+  if (len >= n && len > cap) len = static_cast<int>(cap);
+  const int64_t reach = static_cast<int64_t>(p.row_tiles) * 2 * (kTcRows >> p.hg_log2);
+  if (q_row < 0 || row < q_row || row - q_row >= n || row - q_row >= reach || len < n ||
+      q_row + static_cast<int64_t>(n) > p.num_tokens)
+    return;
+  constexpr int kPer = D / 32;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldg(p.ws_ml + (s * rows + idx) * 2));
+  float num[kPer] = {}, den = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml + (s * rows + idx) * 2));
+    if (ml.y == 0.f) continue;  // no key of weight; its O was not written, perhaps (a sum of NaN goes on)
+    const float f = fast_exp2(ml.x - m);
+    den += f * ml.y;
+    const float* o = p.ws_o + (s * rows + idx) * D + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) num[i] += f * __ldg(o + i);
+  }
+  T* out = static_cast<T*>(p.out) + idx * D + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) out[i] = DType<T>::from_float(den == 0.f ? 0.f : num[i] / den);  // NaN stays
+}
+
+int device_sms() {
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!cached[dev]) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev] = n > 0 ? n : 1;
+  }
+  return cached[dev];
+}
+
+// Pieces that each item's keys are cut into: what makes the rounds of CTAs
+// times a piece's tiles least, three tiles' time counted for a piece's start
+// and end and two for the join.  The items and tiles are the most that the
+// arguments allow for (the lengths are on the device).  Measured: RULE_TEXT
+struct RlPlan {
+  int hg_log2, splits;
+  int64_t items;  // without pieces
+};
+RlPlan rl_plan(int64_t num_tokens, int num_seqs, int group, int num_heads, int block_size, int max_blocks,
+               int max_query_len, int window, bool intervals) {
+  RlPlan pl{0, 1, 0};
+  while (pl.hg_log2 < 3 && group % (2 << pl.hg_log2) == 0) ++pl.hg_log2;
+  const int64_t tokens = 2 * (kTcRows >> pl.hg_log2);  // chunk tokens of an item
+  const int64_t longest = std::min<int64_t>(max_query_len, num_tokens);
+  const int64_t pairs = std::min((longest + tokens - 1) / tokens * num_seqs, num_tokens / tokens + num_seqs);
+  pl.items = pairs * (num_heads >> pl.hg_log2);
+  int64_t keys = static_cast<int64_t>(max_blocks) * block_size;
+  if (window > 0 && !intervals) keys = std::min<int64_t>(keys, window + tokens);
+  const int64_t tiles = (keys + kTcKeys - 1) / kTcKeys + 1, sms = device_sms();
+  int64_t best = 0;
+  for (int s = 1; s <= 32 && 2 * s <= std::max<int64_t>(tiles, 2); ++s) {
+    const int64_t cost = (pl.items * s + sms - 1) / sms * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 : 0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      pl.splits = s;
+    }
+  }
+  return pl;
+}
+
+int64_t rl_workspace(const RlPlan& pl, int64_t num_tokens, int num_heads, int head_dim) {
+  return pl.splits > 1 ? pl.splits * num_tokens * num_heads * (head_dim + 2) * 4 : 0;
+}
+
 template <typename T, int D, bool CAP, bool BIAS>
 cudaError_t launch_rules(const RulesPrefillParams& p, int max_query_len, const CUtensorMap& mq, const CUtensorMap& mk,
                          const CUtensorMap& mv, cudaStream_t st) {
   constexpr int kSmem = RlLayout<D>::kSmem;
   auto kern = prefill_rules_kernel<T, D, CAP, BIAS>;
-  static int sms[64] = {0};  // per device, set once the kernel may use its shared memory there
+  static bool ready[64] = {false};  // per device: the kernel may use its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!sms[dev]) {
+  if (!ready[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    int n = 0;
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    sms[dev] = n > 0 ? n : 1;
+    ready[dev] = true;
   }
   const int tokens = 2 * (kTcRows >> p.hg_log2);  // chunk tokens of an item
   const int64_t pairs = (static_cast<int64_t>(max_query_len) + tokens - 1) / tokens;
-  const int64_t items = pairs * (p.num_heads >> p.hg_log2) * p.num_seqs;
-  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t items = pairs * (p.num_heads >> p.hg_log2) * p.num_seqs * p.splits;
+  if (pairs > INT32_MAX) return cudaErrorInvalidConfiguration;
   RulesPrefillParams a = p;
   a.row_tiles = static_cast<int32_t>(pairs);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sms[dev]));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, device_sms()));
   kern<<<grid, kRlThreads, kSmem, st>>>(a, mq, mk, mv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits <= 1) return e;
+  const int64_t rows = p.num_tokens * p.num_heads;
+  if (rows > static_cast<int64_t>(INT32_MAX) * 4) return cudaErrorInvalidConfiguration;
+  join_pieces_kernel<T, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -806,12 +939,29 @@ cudaError_t launch_rules_form(const RulesPrefillParams& p, int max_query_len, co
 
 using namespace pagedkv;
 
+extern "C" int paged_prefill_rules_workspace_size(int64_t num_query_tokens, int32_t num_seqs, int32_t num_heads,
+                                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                                  int32_t max_blocks_per_seq, int32_t max_query_len, int32_t window,
+                                                  int32_t intervals, size_t* bytes_out) {
+  if (!bytes_out || num_query_tokens < 0 || num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+      num_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128) || block_size <= 0 ||
+      max_blocks_per_seq <= 0 || max_query_len < 0 || window < 0)
+    return KV_ERR_INVALID_ARG;
+  *bytes_out = 0;
+  if (num_query_tokens == 0 || num_seqs == 0 || max_query_len == 0 || !tc_supported(block_size)) return KV_OK;
+  const RlPlan pl = rl_plan(num_query_tokens, num_seqs, num_heads / num_kv_heads, num_heads, block_size,
+                            max_blocks_per_seq, max_query_len, window, intervals != 0);
+  *bytes_out = static_cast<size_t>(rl_workspace(pl, num_query_tokens, num_heads, head_dim));
+  return KV_OK;
+}
+
 extern "C" int paged_prefill_attention_rules(
     void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
     const int32_t* seq_lens, const int32_t* query_start_loc, int64_t num_query_tokens, int32_t num_seqs,
     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,
     int32_t max_blocks_per_seq, int32_t max_query_len, float scale, float softcap, const float* slopes, int32_t window,
-    const int32_t* key_begin, const int32_t* key_end, int dtype, void* stream) {
+    const int32_t* key_begin, const int32_t* key_end, int dtype, void* workspace, size_t workspace_bytes,
+    void* stream) {
   RulesPrefillParams p{};
   int s = make_rules(scale, softcap, slopes, window, key_begin, key_end, &p.rules);
   if (s != KV_OK) return s;
@@ -826,7 +976,18 @@ extern "C" int paged_prefill_attention_rules(
     return cuda_status(e);
   }
   p.test_skip = debug_skip_tile();
-  while (p.hg_log2 < 3 && p.group % (2 << p.hg_log2) == 0) ++p.hg_log2;
+  const RlPlan pl = rl_plan(num_query_tokens, num_seqs, p.group, num_heads, block_size, max_blocks_per_seq,
+                            max_query_len, window, key_begin != nullptr || key_end != nullptr);
+  p.hg_log2 = pl.hg_log2;
+  p.splits = 1;
+  const size_t need = static_cast<size_t>(rl_workspace(pl, num_query_tokens, num_heads, head_dim));
+  if (workspace && need > 0) {
+    if (workspace_bytes < need) return KV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KV_ERR_INVALID_ARG;
+    p.splits = pl.splits;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = p.ws_o + pl.splits * num_query_tokens * num_heads * head_dim;
+  }
   CUtensorMap mq, mk, mv;
   const int64_t rows = num_blocks * block_size;
   if (!tc_map(q, head_dim, num_heads, num_query_tokens, 1 << p.hg_log2, kTcRows >> p.hg_log2, &mq) ||

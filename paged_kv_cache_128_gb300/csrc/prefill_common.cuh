@@ -41,6 +41,12 @@ struct PrefillParams {
 struct RulesPrefillParams : PrefillParams {
   static constexpr bool kRules = true;
   ScoreRules rules;
+  // tensor-core kernel: pieces that an item's keys are cut into, each piece's
+  // unnormalised outputs [splits][num_tokens num_heads][D] and (reference, sum)
+  // of the weights (unused with one)
+  int32_t splits;
+  float* ws_o;
+  float* ws_ml;
 };
 
 // Byte offset of (key, dim) in a [kPfKeys][D] 16-bit tile: 128-byte slabs of

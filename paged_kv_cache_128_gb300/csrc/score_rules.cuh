@@ -152,6 +152,7 @@ template <int NS, int NG, bool CAP>
 __device__ __forceinline__ void rule_scores(const TileRules<NG, CAP>& r, float (&sc)[NS][NG][4], float scale_log2,
                                             int t0) {
   const CapPoly& cap = r.poly;
+  const float from = static_cast<float>(r.pos - t0);  // distance of the first token
   const uint64_t sl2 = tc::f2(scale_log2, scale_log2);
   if constexpr (CAP) {
     // Scores beyond the cap (or in slots that are not seen, at a cost in time
@@ -170,7 +171,7 @@ __device__ __forceinline__ void rule_scores(const TileRules<NG, CAP>& r, float (
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float away = static_cast<float>(r.pos - t0 - u * 16 - (e >> 1) * 8);
+            const float away = from - (u * 16 + (e >> 1) * 8);
             const float2 fall = tc::f2_split(r.fall[ng]);
             sc[u][ng][e] = fmaf(e & 1 ? fall.y : fall.x, away,
                                 soft_cap_far(sc[u][ng][e], scale_log2, r.cap_log2, r.cap_arg));
@@ -182,7 +183,7 @@ __device__ __forceinline__ void rule_scores(const TileRules<NG, CAP>& r, float (
   for (int u = 0; u < NS; ++u)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float away = static_cast<float>(r.pos - t0 - u * 16 - h * 8);
+      const float away = from - (u * 16 + h * 8);
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng) {
         float* d = &sc[u][ng][2 * h];

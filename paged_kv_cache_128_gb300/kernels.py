@@ -514,11 +514,25 @@ def paged_prefill_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
     return out
 
 
+def prefill_rules_workspace(num_tokens: int, num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                            block_size: int, max_blocks: int, max_query_len: int, device, window: int = 0,
+                            intervals: bool = False) -> Optional[torch.Tensor]:
+    """Workspace of ``paged_prefill_attention_rules`` for these sizes (None
+    when it needs none); ``max_blocks``: columns of the block table,
+    ``intervals``: whether the call gives ``key_begin`` or ``key_end``."""
+    n = ctypes.c_size_t()
+    check(lib().paged_prefill_rules_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                   max_blocks, max_query_len, window, 1 if intervals else 0,
+                                                   ctypes.byref(n)), "paged_prefill_rules_workspace_size")
+    return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+
+
 def paged_prefill_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                   block_tables: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
                                   scale: float, max_query_len: int, *, softcap: float = 0.0,
                                   slopes: Optional[torch.Tensor] = None, window: int = 0,
                                   key_begin: Optional[torch.Tensor] = None, key_end: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None,
                                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """``paged_prefill_attention`` under score rules.  Row r of q, at position
     i of a sequence of L tokens, gives key j the score ``s = scale q.k_j``,
@@ -530,7 +544,9 @@ def paged_prefill_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: t
     ``key_end`` past the row's own position lets it see ahead (a prefix, an
     image), ``key_begin`` the start of its document.  A row that sees no key
     gets zeros.  Blocks that end before the first key a tile of rows sees are
-    not looked up."""
+    not looked up.  ``workspace``: ``prefill_rules_workspace(...)`` of these
+    sizes (allocated here if omitted), for calls whose few rows see many keys,
+    which are cut into pieces then; an empty tensor: they are not."""
     dev = q.get_device()
     _check_device(dev, (q, out, k_cache, v_cache, block_tables, seq_lens, query_start_loc),
                   "q out k_cache v_cache block_tables seq_lens query_start_loc")
@@ -553,13 +569,21 @@ def paged_prefill_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: t
         with torch.cuda.device(dev):
             return paged_prefill_attention_rules(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
                                                  scale, max_query_len, softcap=softcap, slopes=slopes, window=window,
-                                                 key_begin=key_begin, key_end=key_end, stream=stream)
+                                                 key_begin=key_begin, key_end=key_end, workspace=workspace,
+                                                 stream=stream)
     cap, sl, win, begin, end = _rules_args(dev, hq, T, softcap, slopes, window, key_begin, key_end)
+    if workspace is None:
+        workspace = _call_workspace(stream, prefill_rules_workspace, T, B, hq, hkv, d, bs, block_tables.shape[1],
+                                    max_query_len, q.device, window, begin is not None or end is not None)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise KVError(1, "workspace must be contiguous on q's device")
+    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
     check(lib().paged_prefill_attention_rules(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), query_start_loc.data_ptr(), T, B, hq, hkv, d, bs, nb, block_tables.shape[1],
-        max_query_len, float(scale), cap, sl, win, begin, end, dtype_code(q.dtype), _stream_ptr(stream)),
-        "paged_prefill_attention_rules")
+        max_query_len, float(scale), cap, sl, win, begin, end, dtype_code(q.dtype), ws_ptr, ws_bytes,
+        _stream_ptr(stream)), "paged_prefill_attention_rules")
     return out
 
 

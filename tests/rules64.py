@@ -142,6 +142,7 @@ class PagedBatch:
         rows = sum(self.chunks)
         self.q = (torch.randn(rows, hq, d, generator=g, device=dev) * q_spread).to(dt)
         self.out = sentinel_tensor((rows, hq, d), dtype, dev)
+        self.uncut = None
         self.scale = 1.0 / math.sqrt(d)
         self.row0 = [0] + np.cumsum(self.chunks).tolist()
         self.start = torch.tensor(self.row0, dtype=torch.int32, device=dev)
@@ -162,8 +163,8 @@ class PagedBatch:
         return out
 
     def check(self, out=None, cap=0.0, slopes=None, window=0, begin=None, end=None, seqs=None):
-        """Every sequence's rows against rules64."""
-        out = self.out if out is None else out
+        """Every sequence's rows against rules64; self.out, and self.uncut if a test has set it, unless `out` is given."""
+        outs = [out] if out is not None else [self.out] if self.uncut is None else [self.out, self.uncut]
         G = self.hq // self.hkv
         for b in range(len(self.lens)) if seqs is None else seqs:
             L, n, r0 = self.lens[b], self.chunks[b], self.row0[b]
@@ -171,7 +172,7 @@ class PagedBatch:
                 continue
             rows = slice(r0, r0 + n)
             if L == 0:
-                assert not out[rows].any(), b
+                assert not any(x[rows].any() for x in outs), b
                 continue
             pos = torch.arange(L - n, L, device="cuda")
             lo = torch.zeros_like(pos) if begin is None else begin[rows].long()
@@ -184,4 +185,5 @@ class PagedBatch:
                 kv = h // G
                 o, tol = rules64(self.q[rows, h], k[:, kv], v[:, kv], self.scale, self.dtype, pos, lo.clamp(min=0), hi, cap,
                                  0.0 if slopes is None else float(slopes[h]), None if vs is None else vs[:, kv])
-                check_rows(out[rows, h], o, tol, (b, h, L))
+                for i, x in enumerate(outs):
+                    check_rows(x[rows, h], o, tol, (i, b, h, L))

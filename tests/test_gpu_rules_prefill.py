@@ -30,9 +30,13 @@ def _batch(dtype, hq, hkv, d, bs, seqs, seed, **over):
 
 
 def _run(t, begin=None, end=None, **rules):
+    """As the wrapper would, which cuts the keys of few rows into pieces, and without pieces (an empty workspace)."""
     pk.device_error()
-    got = pk.paged_prefill_attention_rules(t.out, t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale,
-                                           max(max(t.chunks), 1), key_begin=begin, key_end=end, **rules)
+    args = (t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale, max(max(t.chunks), 1))
+    got = pk.paged_prefill_attention_rules(t.out, *args, key_begin=begin, key_end=end, **rules)
+    t.uncut = torch.full_like(t.out, float("nan"))
+    pk.paged_prefill_attention_rules(t.uncut, *args, key_begin=begin, key_end=end, **rules,
+                                     workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert got is t.out and pk.device_error() == 0
 
 
@@ -207,7 +211,7 @@ def test_captured_and_replayed():
         t.out.fill_(float("nan"))
         graph.replay()
         torch.cuda.synchronize()
-        t.check(cap=15.0, end=end)
+        t.check(out=t.out, cap=15.0, end=end)
     assert pk.device_error() == 0
 
 
@@ -224,3 +228,75 @@ def test_bad_lengths_are_recorded():
     pk.paged_prefill_attention_rules(t.out, t.q, t.kc, t.vc, t.tables, t.seq_lens, start, t.scale, 40, window=8)
     assert pk.device_error() == 8
     assert pk.device_error() == 0
+
+
+def test_many_sequences_of_every_size():
+    """A mixed step: 150 sequences, most of one token, some of none, a few chunks among them."""
+    g = torch.Generator().manual_seed(3)
+    seqs = []
+    for i in range(150):
+        hist = int(torch.randint(0, 400, (1,), generator=g))
+        seqs.append((hist + 1, 0) if i % 7 == 3 else (hist, 300 + i) if i in (31, 32, 90) else (hist, 1 + (i % 5 == 0) * 9))
+    t = _batch("bf16", 8, 2, 128, 16, seqs, seed=10)
+    t.out.fill_(float("nan"))
+    slopes = _slopes(8)
+    _run(t, softcap=15.0, slopes=slopes, window=250)
+    t.check(cap=15.0, slopes=slopes, window=250)
+
+
+def test_same_call_same_bits_and_two_streams_at_once():
+    a = _batch("bf16", 8, 2, 128, 16, [(900, 300), (0, 500)], seed=1)
+    b = _batch("f16", 12, 4, 64, 32, [(100, 800), (50, 77)], seed=2)
+    calls = [(a, dict(softcap=20.0, window=300)), (b, dict(slopes=_slopes(12)))]
+    for t, kw in calls:
+        _run(t, **kw)
+    want = [t.out.clone() for t, _ in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        for t, _ in calls:
+            t.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for (t, kw), s in zip(calls, streams):
+            pk.paged_prefill_attention_rules(t.out, t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale, max(t.chunks),
+                                             stream=s, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.out, w) for (t, _), w in zip(calls, want))
+    assert pk.device_error() == 0
+
+
+@pytest.mark.parametrize("bs", [16, 8])
+def test_chunks_longer_than_max_query_len_are_recorded(bs):
+    t = _batch("bf16", 8, 2, 128, bs, [(0, 300), (20, 50)], seed=3)
+    t.out.fill_(7.0)
+    pk.device_error()
+    pk.paged_prefill_attention_rules(t.out, t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale, 64, window=90)
+    assert pk.device_error() == 8
+    t.check(window=90, seqs=[1])
+    assert bool((t.out[200:300] == 7.0).all())            # past the reach: as they were
+
+
+@pytest.mark.parametrize("shape", [("bf16", 32, 8, 128, 16), ("f16", 8, 1, 128, 32), ("bf16", 14, 2, 64, 16)], ids=str)
+@pytest.mark.parametrize("window", [0, 5000])
+def test_few_rows_over_many_keys(shape, window):
+    """A short chunk after a long history: the keys are cut into pieces.  Rows that see all of them, only the newest or
+    none; a workspace of the caller's that held NaN."""
+    seqs = [(20000, 40), (9000, 3), (5, 1)]
+    t = _batch(*shape, seqs, seed=6)
+    slopes = _slopes(t.hq)
+    _run(t, softcap=30.0, slopes=slopes, window=window)
+    t.check(cap=30.0, slopes=slopes, window=window)
+    begin = torch.zeros(44, dtype=torch.int32, device="cuda")
+    begin[10:20] = 20005
+    begin[20:23] = 20041
+    begin[40] = 8990
+    args = (t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale, 40)
+    ws = pk.prefill_rules_workspace(44, 3, t.hq, t.hkv, t.d, t.bs, t.tables.shape[1], 40, "cuda", window, True)
+    assert ws is not None
+    ws.fill_(0xFF)
+    pk.paged_prefill_attention_rules(t.out, *args, window=window, key_begin=begin, workspace=ws)
+    t.check(out=t.out, window=window, begin=begin)
+    assert not t.out[20:23].any() and pk.device_error() == 0
+    with pytest.raises(pk.KVError) as e:
+        pk.paged_prefill_attention_rules(t.out, *args, window=window, key_begin=begin, workspace=ws[:-16])
+    assert e.value.code == "WORKSPACE"

@@ -23,7 +23,7 @@ CALLS = {
                                          "max_seq_len": 32, **RULES, **END},
     "paged_prefill_attention_rules": {**CACHES, "block_tables": PTR, "seq_lens": PTR, "query_start_loc": PTR,
                                       "num_query_tokens": 0, "num_seqs": 0, **SIZES, "max_query_len": 8, **RULES,
-                                      "key_end": None, "dtype": 2, "stream": None},
+                                      "key_end": None, **END},
 }
 
 
