@@ -528,7 +528,8 @@ int paged_prefill_attention(void* out, const void* q, const void* k_cache, const
  *   workspace: where few rows see many keys, the keys are cut into pieces that
  *     several CTAs take, joined in order; their parts lie here, device memory of
  *     paged_prefill_rules_workspace_size bytes, 16-byte aligned, whose contents
- *     need not be kept.  NULL: the keys are not cut.
+ *     need not be kept; calls that overlap need one each.  NULL: the keys are
+ *     not cut.
  * Other arguments and rules are those of paged_prefill_attention. */
 int paged_prefill_attention_rules(void* out, const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* block_tables, const int32_t* seq_lens,

@@ -83,10 +83,18 @@ struct RlItem {
   int ctx, len;     // positions before the chunk, and in all
   int tok0, head0;  // first chunk token of the pair, first head of the group
   int key_lo, key_hi;          // keys that some row of the pair sees
-  int piece, first, end;       // the piece of them that this is, its tiles first down to end (none: first < end)
+  int pieces, piece;           // what they are cut into, and which of it this is
+  int first, end;              // its tiles, first down to end (none: first < end)
   int tile_lo[2], tile_hi[2];  // key tiles of each query tile in the piece (none: equal)
   int tile0;                   // tiles before the item's first
 };
+
+// What a launch costs, in key tiles, when `items` of `tiles` each are cut into n
+// pieces: the rounds of CTAs times a piece's tiles, three more for its start
+// and end, and two for the join.
+__host__ __device__ inline int64_t rl_cost(int64_t items, int64_t tiles, int64_t n, int64_t ctas) {
+  return (items * n + ctas - 1) / ctas * ((tiles + n - 1) / n + 3) + (n > 1 ? 2 : 0);
+}
 
 // The key tiles of an item as they are walked: first down to end, of which
 // own() says whether query tile q needs one, other() whether the other one does.
@@ -281,30 +289,56 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // grid, ..., every other round in reverse, so that the sums even out.
       // Sequences are looked at 32 at a time, a lane each, and once: what has
       // no rows has no items, whatever max_query_len allows for.
-      const int64_t per_pair = static_cast<int64_t>(ngroups) * p.splits;
+      const int reach = p.row_tiles * 2 * tpt;
+      // lane's sequence: first row, rows, length, pairs of row tiles (0 of a bad one)
+      int my_row = 0, my_n = 0, my_len = 0, my_pairs = 0;
+      auto look = [&](int seq, bool report) {
+        my_row = my_n = my_len = my_pairs = 0;
+        if (seq >= p.num_seqs) return;
+        my_row = __ldg(p.query_start + seq);
+        my_n = __ldg(p.query_start + seq + 1) - my_row;
+        my_len = __ldg(p.seq_lens + seq);
+        const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+        // rows past the reach of max_query_len are left uncomputed; the chunk must
+        // lie inside its sequence and in q, the sequence in its table row
+        const bool bad =
+            my_n > 0 && (my_len < my_n || my_row < 0 || my_row + static_cast<int64_t>(my_n) > p.num_tokens);
+        if (report && (bad || (my_n > 0 && (my_n > reach || my_len > cap)))) record_error(KV_ERR_DEVICE_BOUNDS);
+        if (my_len > cap) my_len = static_cast<int>(cap);
+        if (bad || my_n < 0 || my_len < my_n) my_n = 0;
+        my_pairs = min(my_n / (2 * tpt) + (my_n % (2 * tpt) != 0), p.row_tiles);
+      };
+      // The pieces of each item's keys: up to those that the workspace has room
+      // for, by the rule of rl_plan on the rows and lengths there are (the host
+      // knows only the width of the table).
+      int splits = 1;
+      if (p.splits > 1) {
+        int pairs = 0, tiles = 0;
+        for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+          look(b0 + lane, false);
+          pairs += my_pairs;
+          int keys = my_len;
+          if (p.rules.window > 0 && !p.rules.key_begin && !p.rules.key_end)
+            keys = static_cast<int>(min(static_cast<int64_t>(keys), p.rules.window + 2 * static_cast<int64_t>(tpt)));
+          if (my_pairs > 0) tiles = max(tiles, (keys + kTcKeys - 1) / kTcKeys);
+        }
+        pairs = __reduce_add_sync(0xffffffffu, pairs);
+        tiles = __reduce_max_sync(0xffffffffu, tiles);
+        const int n = lane + 1;
+        const int64_t cost = rl_cost(static_cast<int64_t>(pairs) * ngroups, tiles, n, gridDim.x);
+        uint32_t key = 0xffffffffu;  // the least cost, and of those the fewest pieces
+        if (n <= p.splits && (n == 1 || 2 * n <= tiles))
+          key = static_cast<uint32_t>(min(cost, static_cast<int64_t>(0x3fffffe))) << 5 | lane;
+        splits = static_cast<int>(__reduce_min_sync(0xffffffffu, key) & 31) + 1;
+        if (blockIdx.x == 0 && lane == 0) *p.ws_pieces = splits;
+      }
+      const int64_t per_pair = static_cast<int64_t>(ngroups) * splits;
       int64_t round = 0, before = 0;  // items of the sequences before this chunk of 32
       auto item_of = [&](int64_t r) {
         return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       };
       for (int b0 = 0; b0 < p.num_seqs && ok; b0 += 32) {
-        const int my_b = b0 + lane;
-        int my_row = 0, my_n = 0, my_len = 0;
-        if (my_b < p.num_seqs) {
-          my_row = __ldg(p.query_start + my_b);
-          my_n = __ldg(p.query_start + my_b + 1) - my_row;
-          my_len = __ldg(p.seq_lens + my_b);
-          const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * bs;
-          // rows past the reach of max_query_len are left uncomputed; the chunk must
-          // lie inside its sequence and in q, the sequence in its table row
-          const bool bad =
-              my_n > 0 && (my_len < my_n || my_row < 0 || my_row + static_cast<int64_t>(my_n) > p.num_tokens);
-          if (blockIdx.x == 0 &&
-              (bad || (my_n > 0 && (my_n > p.row_tiles * 2 * static_cast<int64_t>(tpt) || my_len > cap))))
-            record_error(KV_ERR_DEVICE_BOUNDS);
-          if (my_len > cap) my_len = static_cast<int>(cap);
-          if (bad || my_len < my_n) my_n = 0;
-        }
-        const int my_pairs = min(max(my_n, 0) / (2 * tpt) + (max(my_n, 0) % (2 * tpt) != 0), p.row_tiles);
+        look(b0 + lane, blockIdx.x == 0);
         int64_t upto = static_cast<int64_t>(my_pairs) * per_pair;  // items up to and with this lane's sequence
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -318,11 +352,12 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           const int src = __ffs(__ballot_sync(0xffffffffu, x < upto)) - 1;  // the lane whose sequence x lies in
           const int pairs = __shfl_sync(0xffffffffu, my_pairs, src);
           const int64_t rel = x - (__shfl_sync(0xffffffffu, upto, src) - static_cast<int64_t>(pairs) * per_pair);
-          const int b = b0 + src, gi = static_cast<int>(rel % per_pair / p.splits);
+          const int b = b0 + src, gi = static_cast<int>(rel % per_pair / splits);
           const int pair = pairs - 1 - static_cast<int>(rel / per_pair);
           RlItem it;
           it.seq = b;
-          it.piece = static_cast<int>(rel % p.splits);
+          it.pieces = splits;
+          it.piece = static_cast<int>(rel % splits);
           it.q_row = __shfl_sync(0xffffffffu, my_row, src);
           it.n = __shfl_sync(0xffffffffu, my_n, src);
           it.len = __shfl_sync(0xffffffffu, my_len, src);
@@ -357,13 +392,15 @@ __global__ void __launch_bounds__(kRlThreads, 1)
             }
           }
           // The piece: an equal share of the tiles, of which each query tile has
-          // what it needs; first and end are tiles that one of them needs.
+          // what it needs; first and end are tiles that one of them needs.  An item
+          // of fewer tiles has fewer pieces, the rest are empty.
           it.first = -1;
           it.end = 0;
           if (it.key_lo < it.key_hi) {
             const int lowest = it.key_lo / kTcKeys, tiles = (it.key_hi + kTcKeys - 1) / kTcKeys - lowest;
-            const int from = lowest + static_cast<int>(static_cast<int64_t>(tiles) * it.piece / p.splits);
-            const int to = lowest + static_cast<int>(static_cast<int64_t>(tiles) * (it.piece + 1) / p.splits);
+            const int pieces = min(splits, max(1, tiles / 2)), at = min(it.piece, pieces);
+            const int from = lowest + static_cast<int>(static_cast<int64_t>(tiles) * at / pieces);
+            const int to = lowest + static_cast<int>(static_cast<int64_t>(tiles) * min(at + 1, pieces) / pieces);
             int end = INT32_MAX;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -553,6 +590,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       const int key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
       const int64_t row = static_cast<int64_t>(items[slot].q_row) + t;
       const int piece = items[slot].piece;
+      const bool whole = items[slot].pieces == 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_free + slot);
       if (last) break;
@@ -758,7 +796,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       T* orow = static_cast<T*>(p.out) + (row * p.num_heads + head) * D + half * (D / 2);
       const int64_t part = static_cast<int64_t>(piece) * p.num_tokens * p.num_heads + row * p.num_heads + head;
       if (!begun) {  // the tile sees no key
-        if (real && p.splits > 1) {
+        if (real && !whole) {
           if (half == 0) *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(-INFINITY, 0.f);
         } else if (real)
           for (int oc = 0; oc < D / 2; oc += 8) *reinterpret_cast<uint4*>(orow + oc) = make_uint4(0, 0, 0, 0);
@@ -772,14 +810,14 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       tc::fence_after();
       const float inv = l > 0.f ? __fdiv_rn(1.f, l) : 0.f;
       const bool store = ok && real;
-      if (p.splits > 1 && store && half == 0)
+      if (!whole && store && half == 0)
         *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(l == 0.f ? -INFINITY : m_ref, l);
 #pragma unroll 1
       for (int oc = 0; oc < D / 2; oc += 32) {
         uint32_t w[32];
         tc::ld_32x32b_x32(tO + oc, w);
         tc::wait_ld();
-        if (p.splits > 1) {  // joined by join_pieces_kernel
+        if (!whole) {  // joined by join_pieces_kernel
           if (store) {
             float4* to = reinterpret_cast<float4*>(p.ws_o + part * D + half * (D / 2) + oc);
 #pragma unroll
@@ -819,6 +857,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
 template <typename T, int D>
 __global__ void __launch_bounds__(128) join_pieces_kernel(const RulesPrefillParams p) {
   const int lane = threadIdx.x & 31;
+  const int splits = *p.ws_pieces;
+  if (splits == 1) return;  // written by the attention kernel
   const int64_t rows = p.num_tokens * p.num_heads;
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (idx >= rows) return;
@@ -839,9 +879,9 @@ __global__ void __launch_bounds__(128) join_pieces_kernel(const RulesPrefillPara
     return;
   constexpr int kPer = D / 32;
   float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldg(p.ws_ml + (s * rows + idx) * 2));
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, __ldg(p.ws_ml + (s * rows + idx) * 2));
   float num[kPer] = {}, den = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml + (s * rows + idx) * 2));
     if (ml.y == 0.f) continue;  // no key of weight; its O was not written, perhaps (a sum of NaN goes on)
     const float f = fast_exp2(ml.x - m);
@@ -868,13 +908,11 @@ int device_sms() {
   return cached[dev];
 }
 
-// Pieces that each item's keys are cut into: what makes the rounds of CTAs
-// times a piece's tiles least, three tiles' time counted for a piece's start
-// and end and two for the join.  The items and tiles are the most that the
-// arguments allow for (the lengths are on the device).  Measured, 32/8 heads of
-// 128, whole and in pieces: 40 rows after 20000 tokens 447 and 50 us (18 pieces),
-// 64 after 2000 43 and 25 (9), 300 after 4000 106 and 54 (3), 4 x 16 after 500
-// 18.8 both (3).
+// Pieces that each item's keys may be cut into: the number of least cost, for
+// the most items and tiles that the arguments allow for (the lengths are on the
+// device, where the scheduler decides by them).  Measured, 32/8 heads of 128,
+// whole and in pieces: 40 rows after 20000 tokens 447 and 49 us (18 pieces), 64
+// after 2000 43 and 27 (9), 300 after 4000 106 and 54 (3).
 struct RlPlan {
   int hg_log2, splits;
   int64_t items;  // without pieces
@@ -892,7 +930,7 @@ RlPlan rl_plan(int64_t num_tokens, int num_seqs, int group, int num_heads, int b
   const int64_t tiles = (keys + kTcKeys - 1) / kTcKeys + 1, sms = device_sms();
   int64_t best = 0;
   for (int s = 1; s <= 32 && 2 * s <= std::max<int64_t>(tiles, 2); ++s) {
-    const int64_t cost = (pl.items * s + sms - 1) / sms * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 : 0);
+    const int64_t cost = rl_cost(pl.items, tiles, s, sms);
     if (s == 1 || cost < best) {
       best = cost;
       pl.splits = s;
@@ -902,7 +940,7 @@ RlPlan rl_plan(int64_t num_tokens, int num_seqs, int group, int num_heads, int b
 }
 
 int64_t rl_workspace(const RlPlan& pl, int64_t num_tokens, int num_heads, int head_dim) {
-  return pl.splits > 1 ? pl.splits * num_tokens * num_heads * (head_dim + 2) * 4 : 0;
+  return pl.splits > 1 ? 16 + pl.splits * num_tokens * num_heads * (head_dim + 2) * 4 : 0;
 }
 
 template <typename T, int D, bool CAP, bool BIAS>
@@ -997,7 +1035,8 @@ extern "C" int paged_prefill_attention_rules(
     if (workspace_bytes < need) return KV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return KV_ERR_INVALID_ARG;
     p.splits = pl.splits;
-    p.ws_o = static_cast<float*>(workspace);
+    p.ws_pieces = static_cast<int32_t*>(workspace);
+    p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + 16);
     p.ws_ml = p.ws_o + pl.splits * num_query_tokens * num_heads * head_dim;
   }
   CUtensorMap mq, mk, mv;

@@ -41,10 +41,11 @@ struct PrefillParams {
 struct RulesPrefillParams : PrefillParams {
   static constexpr bool kRules = true;
   ScoreRules rules;
-  // tensor-core kernel: pieces that an item's keys are cut into, each piece's
-  // unnormalised outputs [splits][num_tokens num_heads][D] and (reference, sum)
-  // of the weights (unused with one)
+  // tensor-core kernel: pieces that an item's keys may be cut into, how many
+  // they are cut into, each piece's unnormalised outputs [splits][num_tokens
+  // num_heads][D] and (reference, sum) of the weights (unused where one is most)
   int32_t splits;
+  int32_t* ws_pieces;
   float* ws_o;
   float* ws_ml;
 };

@@ -520,6 +520,11 @@ def prefill_rules_workspace(num_tokens: int, num_seqs: int, num_heads: int, num_
     """Workspace of ``paged_prefill_attention_rules`` for these sizes (None
     when it needs none); ``max_blocks``: columns of the block table,
     ``intervals``: whether the call gives ``key_begin`` or ``key_end``."""
+    index = torch.device(device).index
+    if index is not None and index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return prefill_rules_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                           max_blocks, max_query_len, device, window, intervals)
     n = ctypes.c_size_t()
     check(lib().paged_prefill_rules_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                                    max_blocks, max_query_len, window, 1 if intervals else 0,
