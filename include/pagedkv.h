@@ -541,12 +541,12 @@ int paged_prefill_attention_rules(void* out, const void* q, const void* k_cache,
                                   void* stream);
 
 /* Workspace bytes of paged_prefill_attention_rules for these arguments (no
- * passage, as there; 0: it needs none).  intervals: whether the call gives
- * key_begin or key_end. */
+ * passage, as there; 0: it needs none).  begins: whether the call gives
+ * key_begin (such calls are not cut). */
 int paged_prefill_rules_workspace_size(int64_t num_query_tokens, int32_t num_seqs, int32_t num_heads,
                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                        int32_t max_blocks_per_seq, int32_t max_query_len, int32_t window,
-                                       int32_t intervals, size_t* bytes_out);
+                                       int32_t begins, size_t* bytes_out);
 
 /* paged_decode_attention with the score rules above (no passage, as there):
  * the query is at position i = seq_lens[b] - 1, key_begin has one entry per

@@ -26,7 +26,7 @@ namespace {
 // of the pair needs is not loaded.  The key tiles are walked from the last to
 // the first: under a falling bias, and in causal attention, a row's largest
 // scores then tend to come first, and the softmax reference, which moves only
-// when a score exceeds it by 2^8, stays where it is.
+// when a tile's weights have outgrown it, stays where it is.
 //
 // Tensor memory (512 columns): S of the two tiles at 0 and 128 (P, two keys to
 // a column, over the upper half of its S), O at 256 and 256 + D.
@@ -89,11 +89,13 @@ struct RlItem {
   int tile0;                   // tiles before the item's first
 };
 
-// What a launch costs, in key tiles, when `items` of `tiles` each are cut into n
-// pieces: the rounds of CTAs times a piece's tiles, three more for its start
-// and end, and two for the join.
-__host__ __device__ inline int64_t rl_cost(int64_t items, int64_t tiles, int64_t n, int64_t ctas) {
-  return (items * n + ctas - 1) / ctas * ((tiles + n - 1) / n + 3) + (n > 1 ? 2 : 0);
+// What a launch costs, in key tiles' time, when items that need `work` tiles
+// together and `longest` at most are cut into n pieces each: the longest piece or
+// the mean of the CTAs, six tiles for a piece's start, end and parts, three for
+// the join.
+__host__ __device__ inline float rl_cost(float items, float work, float longest, int n, float ctas) {
+  const float piece = longest / n + 6.f, mean = (work + 6.f * items * n) / ctas;
+  return (piece > mean ? piece : mean) + (n > 1 ? 3.f : 0.f);
 }
 
 // The key tiles of an item as they are walked: first down to end, of which
@@ -313,22 +315,28 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // knows only the width of the table).
       int splits = 1;
       if (p.splits > 1) {
-        int pairs = 0, tiles = 0;
+        float items = 0.f, work = 0.f, longest = 0.f;
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
           look(b0 + lane, false);
-          pairs += my_pairs;
-          int keys = my_len;
-          if (p.rules.window > 0 && !p.rules.key_begin && !p.rules.key_end)
-            keys = static_cast<int>(min(static_cast<int64_t>(keys), p.rules.window + 2 * static_cast<int64_t>(tpt)));
-          if (my_pairs > 0) tiles = max(tiles, (keys + kTcKeys - 1) / kTcKeys);
+          // keys of the sequence's last pair of row tiles and of its first
+          int64_t most = my_len, least = my_len - my_n + 2 * tpt;
+          if (p.rules.window > 0) most = min(most, p.rules.window + 2 * static_cast<int64_t>(tpt));
+          least = min(least, most);
+          const float last = static_cast<float>((most + kTcKeys - 1) / kTcKeys);
+          items += my_pairs;
+          work += my_pairs * 0.5f * (last + static_cast<float>((least + kTcKeys - 1) / kTcKeys));
+          if (my_pairs > 0) longest = fmaxf(longest, last);
         }
-        pairs = __reduce_add_sync(0xffffffffu, pairs);
-        tiles = __reduce_max_sync(0xffffffffu, tiles);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          items += __shfl_xor_sync(0xffffffffu, items, off);
+          work += __shfl_xor_sync(0xffffffffu, work, off);
+          longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, off));
+        }
         const int n = lane + 1;
-        const int64_t cost = rl_cost(static_cast<int64_t>(pairs) * ngroups, tiles, n, gridDim.x);
-        uint32_t key = 0xffffffffu;  // the least cost, and of those the fewest pieces
-        if (n <= p.splits && (n == 1 || 2 * n <= tiles))
-          key = static_cast<uint32_t>(min(cost, static_cast<int64_t>(0x3fffffe))) << 5 | lane;
+        uint32_t key = 0xffffffffu;  // the least cost (positive: in the order of its bits), then the fewest pieces
+        if (n <= p.splits && (n == 1 || 2 * n <= longest))
+          key = (__float_as_uint(rl_cost(items * ngroups, work * ngroups, longest, n, gridDim.x)) & ~31u) | lane;
         splits = static_cast<int>(__reduce_min_sync(0xffffffffu, key) & 31) + 1;
         if (blockIdx.x == 0 && lane == 0) *p.ws_pieces = splits;
       }
@@ -744,7 +752,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         weigh();
         // Do the row's two warps agree that the reference holds?  The barrier
         // also says that both have read S, which P goes over.
-        if (barrier_or(pair, 64, sum > kGrown)) {
+        tc::fence_before();
+        const bool grown = barrier_or(pair, 64, sum > kGrown);
+        tc::fence_after();
+        if (grown) {
           const float m = row_max();
           const float m_new = fmaxf(m_ref, m), alpha = fast_exp2(m_ref - m_new);
           l *= alpha;
@@ -767,7 +778,9 @@ __global__ void __launch_bounds__(kRlThreads, 1)
             }
           }
           weigh();
+          tc::fence_before();
           named_barrier_sync(pair, 64);
+          tc::fence_after();
         }
         tc::st_32x32b_x32(tS + 64 + 32 * half, pk);
         l += sum;
@@ -908,32 +921,35 @@ int device_sms() {
   return cached[dev];
 }
 
-// Pieces that each item's keys may be cut into: the number of least cost, for
+// Pieces that each item's keys may be cut into: the number of least cost for
 // the most items and tiles that the arguments allow for (the lengths are on the
-// device, where the scheduler decides by them).  Measured, 32/8 heads of 128,
-// whole and in pieces: 40 rows after 20000 tokens 447 and 49 us (18 pieces), 64
-// after 2000 43 and 27 (9), 300 after 4000 106 and 54 (3).
+// device, where the scheduler decides by them, up to this number).  Measured,
+// 32/8 heads of 128, whole and in pieces: 40 rows after 20000 tokens 445 and 50
+// us (19 pieces), 64 after 2000 43 and 27 (8), 300 after 4000 105 and 62 (4), 1000
+// after 8000 209 and 159 (2); 2600 causal rows of 16/2 heads 60, and 79 in 3
+// pieces, which this cost does not call for.  Calls that give key_begin are not
+// cut: what their rows see has little to do with the lengths.
 struct RlPlan {
   int hg_log2, splits;
-  int64_t items;  // without pieces
 };
 RlPlan rl_plan(int64_t num_tokens, int num_seqs, int group, int num_heads, int block_size, int max_blocks,
-               int max_query_len, int window, bool intervals) {
-  RlPlan pl{0, 1, 0};
+               int max_query_len, int window, bool begins) {
+  RlPlan pl{0, 1};
   while (pl.hg_log2 < 3 && group % (2 << pl.hg_log2) == 0) ++pl.hg_log2;
+  if (begins) return pl;
   const int64_t tokens = 2 * (kTcRows >> pl.hg_log2);  // chunk tokens of an item
   const int64_t longest = std::min<int64_t>(max_query_len, num_tokens);
   const int64_t pairs = std::min((longest + tokens - 1) / tokens * num_seqs, num_tokens / tokens + num_seqs);
-  pl.items = pairs * (num_heads >> pl.hg_log2);
+  const int64_t items = pairs * (num_heads >> pl.hg_log2);
   int64_t keys = static_cast<int64_t>(max_blocks) * block_size;
-  if (window > 0 && !intervals) keys = std::min<int64_t>(keys, window + tokens);
-  const int64_t tiles = (keys + kTcKeys - 1) / kTcKeys + 1, sms = device_sms();
-  int64_t best = 0;
-  for (int s = 1; s <= 32 && 2 * s <= std::max<int64_t>(tiles, 2); ++s) {
-    const int64_t cost = rl_cost(pl.items, tiles, s, sms);
-    if (s == 1 || cost < best) {
+  if (window > 0) keys = std::min<int64_t>(keys, window + tokens);
+  const int64_t tiles = (keys + kTcKeys - 1) / kTcKeys;
+  float best = 0.f;
+  for (int n = 1; n <= 32 && (n == 1 || 2 * n <= tiles); ++n) {
+    const float cost = rl_cost(items, static_cast<float>(items) * tiles, tiles, n, device_sms());
+    if (n == 1 || cost < best) {
       best = cost;
-      pl.splits = s;
+      pl.splits = n;
     }
   }
   return pl;
@@ -992,7 +1008,7 @@ using namespace pagedkv;
 extern "C" int paged_prefill_rules_workspace_size(int64_t num_query_tokens, int32_t num_seqs, int32_t num_heads,
                                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                                   int32_t max_blocks_per_seq, int32_t max_query_len, int32_t window,
-                                                  int32_t intervals, size_t* bytes_out) {
+                                                  int32_t begins, size_t* bytes_out) {
   if (!bytes_out || num_query_tokens < 0 || num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
       num_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128) || block_size <= 0 ||
       max_blocks_per_seq <= 0 || max_query_len < 0 || window < 0)
@@ -1000,7 +1016,7 @@ extern "C" int paged_prefill_rules_workspace_size(int64_t num_query_tokens, int3
   *bytes_out = 0;
   if (num_query_tokens == 0 || num_seqs == 0 || max_query_len == 0 || !tc_supported(block_size)) return KV_OK;
   const RlPlan pl = rl_plan(num_query_tokens, num_seqs, num_heads / num_kv_heads, num_heads, block_size,
-                            max_blocks_per_seq, max_query_len, window, intervals != 0);
+                            max_blocks_per_seq, max_query_len, window, begins != 0);
   *bytes_out = static_cast<size_t>(rl_workspace(pl, num_query_tokens, num_heads, head_dim));
   return KV_OK;
 }
@@ -1027,7 +1043,7 @@ extern "C" int paged_prefill_attention_rules(
   }
   p.test_skip = debug_skip_tile();
   const RlPlan pl = rl_plan(num_query_tokens, num_seqs, p.group, num_heads, block_size, max_blocks_per_seq,
-                            max_query_len, window, key_begin != nullptr || key_end != nullptr);
+                            max_query_len, window, key_begin != nullptr);
   p.hg_log2 = pl.hg_log2;
   p.splits = 1;
   const size_t need = static_cast<size_t>(rl_workspace(pl, num_query_tokens, num_heads, head_dim));

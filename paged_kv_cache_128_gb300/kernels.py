@@ -516,18 +516,18 @@ def paged_prefill_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
 
 def prefill_rules_workspace(num_tokens: int, num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                             block_size: int, max_blocks: int, max_query_len: int, device, window: int = 0,
-                            intervals: bool = False) -> Optional[torch.Tensor]:
+                            begins: bool = False) -> Optional[torch.Tensor]:
     """Workspace of ``paged_prefill_attention_rules`` for these sizes (None
     when it needs none); ``max_blocks``: columns of the block table,
-    ``intervals``: whether the call gives ``key_begin`` or ``key_end``."""
+    ``begins``: whether the call gives ``key_begin`` (its keys are not cut then)."""
     index = torch.device(device).index
     if index is not None and index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return prefill_rules_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                                           max_blocks, max_query_len, device, window, intervals)
+                                           max_blocks, max_query_len, device, window, begins)
     n = ctypes.c_size_t()
     check(lib().paged_prefill_rules_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                                                   max_blocks, max_query_len, window, 1 if intervals else 0,
+                                                   max_blocks, max_query_len, window, 1 if begins else 0,
                                                    ctypes.byref(n)), "paged_prefill_rules_workspace_size")
     return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
 
@@ -579,7 +579,7 @@ def paged_prefill_attention_rules(out: torch.Tensor, q: torch.Tensor, k_cache: t
     cap, sl, win, begin, end = _rules_args(dev, hq, T, softcap, slopes, window, key_begin, key_end)
     if workspace is None:
         workspace = _call_workspace(stream, prefill_rules_workspace, T, B, hq, hkv, d, bs, block_tables.shape[1],
-                                    max_query_len, q.device, window, begin is not None or end is not None)
+                                    max_query_len, q.device, window, begin is not None)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise KVError(1, "workspace must be contiguous on q's device")
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \

@@ -286,17 +286,19 @@ def test_few_rows_over_many_keys(shape, window):
     slopes = _slopes(t.hq)
     _run(t, softcap=30.0, slopes=slopes, window=window)
     t.check(cap=30.0, slopes=slopes, window=window)
-    begin = torch.zeros(44, dtype=torch.int32, device="cuda")
-    begin[10:20] = 20005
-    begin[20:23] = 20041
-    begin[40] = 8990
+    end = (_positions(t) + 1).to(torch.int32)
+    end[10:20] = 37                                        # among the oldest keys: most pieces hold no key of theirs
+    end[20:23] = 0
+    end[40] = 9003
     args = (t.q, t.kc, t.vc, t.tables, t.seq_lens, t.start, t.scale, 40)
-    ws = pk.prefill_rules_workspace(44, 3, t.hq, t.hkv, t.d, t.bs, t.tables.shape[1], 40, "cuda", window, True)
+    ws = pk.prefill_rules_workspace(44, 3, t.hq, t.hkv, t.d, t.bs, t.tables.shape[1], 40, "cuda", window)
     assert ws is not None
     ws.fill_(0xFF)
-    pk.paged_prefill_attention_rules(t.out, *args, window=window, key_begin=begin, workspace=ws)
-    t.check(out=t.out, window=window, begin=begin)
+    pk.paged_prefill_attention_rules(t.out, *args, window=window, key_end=end, workspace=ws)
+    assert int(ws[:4].view(torch.int32)[0]) > 1            # it was cut
+    t.check(out=t.out, window=window, end=end)
     assert not t.out[20:23].any() and pk.device_error() == 0
     with pytest.raises(pk.KVError) as e:
-        pk.paged_prefill_attention_rules(t.out, *args, window=window, key_begin=begin, workspace=ws[:-16])
+        pk.paged_prefill_attention_rules(t.out, *args, window=window, key_end=end, workspace=ws[:-16])
     assert e.value.code == "WORKSPACE"
+    assert pk.prefill_rules_workspace(44, 3, t.hq, t.hkv, t.d, t.bs, t.tables.shape[1], 40, "cuda", window, True) is None
