@@ -82,7 +82,8 @@ inline int make_rules(float scale, float softcap, const float* slopes, int32_t w
 }
 
 // The keys lo .. hi - 1 that query row `row`, at position i of L tokens, sees
-// (none: hi <= lo).
+// (none: hi <= lo).  Both are 0 or more whatever the arrays hold, so that taking
+// a position of the sequence from them stays in 32 bits.
 struct KeySpan {
   int lo, hi;
 };
@@ -91,7 +92,7 @@ __device__ __forceinline__ KeySpan keys_seen(const ScoreRules& r, int64_t row, i
   if (r.window > 0) s.lo = max(0, i - r.window + 1);
   if (r.key_begin) s.lo = max(s.lo, __ldg(r.key_begin + row));
   if (r.key_end) s.hi = __ldg(r.key_end + row);
-  s.hi = min(s.hi, L);
+  s.hi = max(0, min(s.hi, L));
   return s;
 }
 
