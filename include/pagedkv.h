@@ -480,7 +480,8 @@ int paged_decode_step_fp8(void* out, const void* q, const void* k, const void* v
  *     or bf16), 16-byte aligned; caches as for paged_decode_attention.
  *   query_start_loc: device int32[num_seqs + 1], non-decreasing, every
  *     entry in [0, num_query_tokens].
- *   max_query_len: host upper bound of the chunk lengths (sizes the grid).
+ *   max_query_len: host upper bound of the chunk lengths (sizes the grid);
+ *     more than num_query_tokens counts as that many.
  *     A longer chunk's rows past the grid's reach are not computed, and the
  *     launch records KV_ERR_DEVICE_BOUNDS.
  *   head_dim 64 or 128.

@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int qs = __ldg(p.query_start + b), n = __ldg(p.query_start + b + 1) - qs;
   // rows past the grid's reach (a chunk longer than max_query_len) would be
   // left uncomputed: the sequence's last row tile in the grid reports it
-  if (qt == nrt - 1 && gi == 0 && threadIdx.x == 0 && n > nrt * tpt) record_error(KV_ERR_DEVICE_BOUNDS);
+  if (qt == nrt - 1 && gi == 0 && threadIdx.x == 0 && n > static_cast<int64_t>(nrt) * tpt)
+    record_error(KV_ERR_DEVICE_BOUNDS);
   const int tok0 = qt * tpt;  // first chunk token of the tile
   if (n <= 0 || tok0 >= n) return;
   int L = __ldg(p.seq_lens + b);
@@ -482,6 +483,7 @@ extern "C" int paged_prefill_attention(void* out, const void* q, const void* k_c
                                num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
                                max_query_len, scale, dtype, &p);
   if (s != KV_OK || p.num_seqs == 0) return s;
+  max_query_len = longest_chunk(max_query_len, num_query_tokens);
   p.test_skip = debug_skip_tile();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!tc_supported(block_size)) {

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       // grid, ..., every other round in reverse, so that the sums even out.
       // Sequences are looked at 32 at a time, a lane each, and once: what has
       // no rows has no items, whatever max_query_len allows for.
-      const int reach = p.row_tiles * 2 * tpt;
+      const int64_t reach = static_cast<int64_t>(p.row_tiles) * 2 * tpt;
       // lane's sequence: first row, rows, length, pairs of row tiles (0 of a bad one)
       int my_row = 0, my_n = 0, my_len = 0, my_pairs = 0;
       auto look = [&](int seq, bool report) {
@@ -1035,6 +1035,7 @@ extern "C" int paged_prefill_attention_rules(
                      num_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_query_len,
                      scale, dtype, &p);
   if (s != KV_OK || p.num_seqs == 0) return s;
+  max_query_len = longest_chunk(max_query_len, num_query_tokens);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!tc_supported(block_size)) {
     const cudaError_t e = dtype == KV_DTYPE_F16 ? launch_prefill<__half>(p, head_dim, max_query_len, st)

@@ -4,6 +4,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
   const int qs = __ldg(p.query_start + b), n = __ldg(p.query_start + b + 1) - qs;
   // rows past the grid's reach (a chunk longer than max_query_len) would be
   // left uncomputed: the last row tile of the sequence reports it
-  if (qt == gridDim.x - 1 && h == 0 && tid == 0 && n > static_cast<int>(gridDim.x) * kPfRows)
+  if (qt == gridDim.x - 1 && h == 0 && tid == 0 && n > static_cast<int64_t>(gridDim.x) * kPfRows)
     record_error(KV_ERR_DEVICE_BOUNDS);
   if (n <= 0 || qt * kPfRows >= n) return;
   if (qs < 0 || qs + n > p.num_tokens) {  // the chunk's rows must lie inside q
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
 
 template <typename T, typename P>
 cudaError_t launch_prefill(const P& p, int head_dim, int max_query_len, cudaStream_t st) {
-  const dim3 grid((max_query_len + kPfRows - 1) / kPfRows, p.num_heads, p.num_seqs);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_query_len) + kPfRows - 1) / kPfRows), p.num_heads,
+                  p.num_seqs);
   if (head_dim == 64) prefill_kernel<T, 64, P><<<grid, kPfWarps * 32, 0, st>>>(p);
   else prefill_kernel<T, 128, P><<<grid, kPfWarps * 32, 0, st>>>(p);
   return cudaGetLastError();
@@ -352,6 +354,12 @@ bool tc_map(const void* base, int64_t n0, int64_t n1, int64_t n2, int box1, int 
 bool tc_supported(int block_size) { return block_size >= 16 && block_size % 16 == 0 && kTcKeys % block_size == 0; }
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
+
+// Rows of the longest chunk: what the caller allows for, and no more than q
+// has (the largest int32 says "no limit"; grids and reaches go by this).
+int32_t longest_chunk(int32_t max_query_len, int64_t num_query_tokens) {
+  return static_cast<int32_t>(std::min<int64_t>(max_query_len, num_query_tokens));
+}
 
 // A call's arguments, checked, as kernel parameters (num_seqs 0: nothing to do).
 int prefill_params(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
