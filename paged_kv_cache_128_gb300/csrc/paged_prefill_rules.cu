@@ -3,6 +3,7 @@
 // seen both ways, each query row over its own interval of keys.
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "prefill_common.cuh"
@@ -629,9 +630,11 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         const uint32_t tSh = tS + 64 * half;
         uint32_t pk[32];  // P, two keys to a column
         float sum;
-        // The row's largest score, over both halves.  The cap grows with the
-        // score, so that without a bias it is taken of the largest alone; with one,
-        // every score is capped, by the polynomial unless one lies beyond it.
+        // The row's largest score, over both halves (-inf: none has a weight).
+        // The cap grows with the score, so that without a bias it is taken of the
+        // largest alone (of the lowest number in the place of -inf, which the cap
+        // gives a weight); with one, every score is capped, by the polynomial unless
+        // one lies beyond it.
         auto row_max = [&]() {
           float m = -INFINITY;
           auto scan = [&](auto in_full) -> bool {
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           if (scan(std::false_type())) {
             if constexpr (CAP && BIAS) scan(std::true_type());
           }
+          if (CAP && !BIAS && lo < min(hi, 64) && hi > 0) m = fmaxf(m, -FLT_MAX);  // a key of this half is seen
           *row_own = m;
           named_barrier_sync(pair, 64);
           m = fmaxf(m, *row_other);
