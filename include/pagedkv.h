@@ -524,8 +524,9 @@ int paged_prefill_attention(void* out, const void* q, const void* k_cache, const
  * Values: a row's weight on a key it does not see is 0, and V there is cleared
  * where no row of a tile (256 / heads consecutive tokens, heads the largest
  * power of two up to 8 that divides num_heads / num_kv_heads; 64 in the mma.sync
- * kernel) sees it; a NaN or infinity in the value of a key that another row of
- * the tile sees can reach the row.
+ * kernel) sees it, between the rows' intervals as well as before and after them;
+ * a NaN or infinity in the value of a key that another row of the tile sees can
+ * reach the row.  Blocks between a tile's first and last seen key are looked up.
  *   workspace: where few rows see many keys, the keys are cut into pieces that
  *     several CTAs take, joined in order; their parts lie here, device memory of
  *     paged_prefill_rules_workspace_size bytes, 16-byte aligned, whose contents

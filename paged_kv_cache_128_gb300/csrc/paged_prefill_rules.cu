@@ -41,7 +41,8 @@ namespace {
 //     run at once and the tensor cores wait for both);
 //   warps 0-7 and 8-15: the softmax of the first and second query tile, half a
 //     row's keys per thread.
-// V rows that lie in no row's interval are cleared before P V reads them.
+// V rows that lie in no row's interval are cleared before P V reads them: the
+// warp that loads a V tile notes which of its keys some row of the pair sees.
 // Where few rows see many keys an item's key tiles are cut into pieces, whose
 // parts join_pieces_kernel joins.
 //
@@ -83,7 +84,9 @@ struct RlItem {
   int q_row, n;     // first row of the sequence's chunk in q, its tokens
   int ctx, len;     // positions before the chunk, and in all
   int tok0, head0;  // first chunk token of the pair, first head of the group
-  int key_lo, key_hi;          // keys that some row of the pair sees
+  int key_lo, key_hi;          // from the first key that some row of the pair sees to the last
+  int gaps;                    // there may be keys between that none sees
+  int whole_lo, whole_hi;      // tiles all of whose keys some row sees (with gaps: none are said to be)
   int pieces, piece;           // what they are cut into, and which of it this is
   int first, end;              // its tiles, first down to end (none: first < end)
   int tile_lo[2], tile_hi[2];  // key tiles of each query tile in the piece (none: equal)
@@ -150,6 +153,26 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool x) {
   return r != 0;
 }
 
+// The rows of a V tile whose bit in `keys` is not set, cleared by 256 threads;
+// out of line, as tiles that need it are few.
+template <int D>
+__device__ __noinline__ void clear_unseen(uint8_t* tile, const uint4* keys, int thread) {
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+  const uint4 m = *keys;
+  const uint32_t words[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (words[w] == 0xffffffffu) continue;
+#pragma unroll
+    for (int i = 0; i < 32 * kChunks; i += 2 * kTcRows) {
+      const int key = (i + thread) / kChunks, rest = thread % kChunks;
+      if (!(words[w] >> key & 1u))
+        *reinterpret_cast<uint4*>(tile + (rest >> 3) * RlLayout<D>::kSlab + (w * 32 + key) * 128 + (rest & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
 template <typename T, int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kRlThreads, 1)
     prefill_rules_kernel(const RulesPrefillParams p, const __grid_constant__ CUtensorMap tmQ,
@@ -172,7 +195,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   uint64_t* bar_end = bar_free + 2;             // after a wait ran out: all MMAs done
   RlItem* items = reinterpret_cast<RlItem*>(bar_end + 1);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
-  static_assert((2 * kRing + 15) * 8 + 2 * sizeof(RlItem) + 4 <= 512, "barrier area");
+  uint4* seen = reinterpret_cast<uint4*>(sm + Lay::kOffBar + 512) - kDeep;  // [kDeep] keys of a V tile that are seen
+  static_assert((2 * kRing + 15) * 8 + 2 * sizeof(RlItem) + 4 <= 512 - kDeep * 16, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hg = 1 << p.hg_log2, tpt = kTcRows >> p.hg_log2;  // heads and tokens of a row tile
@@ -238,7 +262,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       }
       return e;
     };
-    auto load = [&](const CUtensorMap* map, int kvh, int e) {
+    auto load = [&](const CUtensorMap* map, int kvh, int e, const uint4& keys) {
       const int slot = (values ? kDeep : 0) + loaded % kDeep;
       if (loaded >= kDeep && !wait(bar_empty + slot, ((loaded / kDeep) - 1) & 1)) return;
       if (!values && p.test_skip >= 0 && blockIdx.x == 0 && loaded == p.test_skip) {
@@ -246,7 +270,10 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         return;
       }
       const int copies = __popc(__ballot_sync(0xffffffffu, e >= 0));
-      if (lane == 0) mbar_arrive_expect_tx(bar_full + slot, static_cast<uint32_t>(copies * bs * 128));
+      if (lane == 0) {
+        if (values) seen[slot - kDeep] = keys;
+        mbar_arrive_expect_tx(bar_full + slot, static_cast<uint32_t>(copies * bs * 128));
+      }
       __syncwarp();
       if (e >= 0)
         tma_load_3d(sm + Lay::kOffRing + slot * Lay::kTile + my_slab * Lay::kSlab + my_blk * bs * 128, map,
@@ -261,15 +288,44 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         const RlSpan walk(items[slot], 0);
         const int seq = items[slot].seq, key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
         const int kvh = items[slot].head0 / p.group;
+        const bool gaps = items[slot].gaps;
+        const int tok0 = items[slot].tok0, rows = min(2 * tpt, items[slot].n - tok0), pos0 = items[slot].ctx + tok0,
+                  len = items[slot].len;
+        const int64_t row0 = static_cast<int64_t>(items[slot].q_row) + tok0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_free + slot);
         if (seq < 0) break;
+        // a bit for each key of tile kt that some row of the pair sees
+        auto seen_in = [&](int kt) {
+          uint4 m = make_uint4(0, 0, 0, 0);
+          auto add = [&](int lo, int hi) {
+            lo -= kt * kTcKeys;
+            hi -= kt * kTcKeys;
+            m.x |= bits_between(lo, hi);
+            m.y |= bits_between(lo - 32, hi - 32);
+            m.z |= bits_between(lo - 64, hi - 64);
+            m.w |= bits_between(lo - 96, hi - 96);
+          };
+          if (!gaps) {
+            add(key_lo, key_hi);
+          } else {
+            for (int t = lane; t < rows; t += 32) {
+              const KeySpan s = keys_seen(p.rules, row0 + t, pos0 + t, len);
+              add(s.lo, s.hi);
+            }
+            m.x = __reduce_or_sync(0xffffffffu, m.x);
+            m.y = __reduce_or_sync(0xffffffffu, m.y);
+            m.z = __reduce_or_sync(0xffffffffu, m.z);
+            m.w = __reduce_or_sync(0xffffffffu, m.w);
+          }
+          return m;
+        };
         int kt = walk.below(walk.first + 1);
         int e = kt >= walk.end ? entry(seq, key_lo, key_hi, kt) : -1;
         while (kt >= walk.end && ok) {
           const int next = walk.below(kt);
           const int e_next = next >= walk.end ? entry(seq, key_lo, key_hi, next) : -1;
-          load(&tmV, kvh, e);
+          load(&tmV, kvh, e, seen_in(kt));
           kt = next;
           e = e_next;
         }
@@ -375,6 +431,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           it.ctx = it.len - it.n;
           it.key_lo = INT32_MAX;
           it.key_hi = 0;
+          it.gaps = 0;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int t0 = it.tok0 + q * tpt, t1 = min(t0 + tpt, it.n);
@@ -386,7 +443,15 @@ __global__ void __launch_bounds__(kRlThreads, 1)
                   lo = min(lo, s.lo);
                   hi = max(hi, s.hi);
                 }
+                // where every row's interval meets the next one's, all keys between
+                // the pair's first and last are seen
+                if (t + 1 < min(it.tok0 + 2 * tpt, it.n)) {
+                  const KeySpan u =
+                      keys_seen(p.rules, static_cast<int64_t>(it.q_row) + t + 1, it.ctx + t + 1, it.len);
+                  if (s.lo >= s.hi || u.lo >= u.hi || s.lo > u.hi || u.lo > s.hi) it.gaps = 1;
+                }
               }
+              it.gaps = __any_sync(0xffffffffu, it.gaps);
               lo = __reduce_min_sync(0xffffffffu, lo);
               hi = __reduce_max_sync(0xffffffffu, hi);
             } else if (t0 < t1) {  // a window's ends move with the row
@@ -405,6 +470,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           // of fewer tiles has fewer pieces, the rest are empty.
           it.first = -1;
           it.end = 0;
+          it.whole_lo = it.gaps ? INT32_MAX : it.key_lo / kTcKeys + (it.key_lo % kTcKeys != 0);
+          it.whole_hi = it.key_hi / kTcKeys;
           if (it.key_lo < it.key_hi) {
             const int lowest = it.key_lo / kTcKeys, tiles = (it.key_hi + kTcKeys - 1) / kTcKeys - lowest;
             const int pieces = min(splits, max(1, tiles / 2)), at = min(it.piece, pieces);
@@ -435,7 +502,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           while (kt >= walk.end && ok) {
             const int next = walk.below(kt);
             const int e_next = next >= walk.end ? entry(b, it.key_lo, it.key_hi, next) : -1;
-            load(&tmK, kvh, e);
+            load(&tmK, kvh, e, make_uint4(0, 0, 0, 0));
             if (first && ok) {  // Q after the first K tile, which waits for less
               first = false;
               if (q_loads > 0 && !wait(bar_qempty, (q_loads - 1) & 1)) break;
@@ -596,7 +663,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       const int t = items[slot].tok0 + tok;
       const bool real = t < items[slot].n;
       const int pos = items[slot].ctx + t, head = items[slot].head0 + hh, len = items[slot].len;
-      const int key_lo = items[slot].key_lo, key_hi = items[slot].key_hi;
+      // tiles whole_lo .. whole_hi - 1 hold no key that no row of the pair sees
+      const int whole_lo = items[slot].whole_lo, whole_hi = items[slot].whole_hi;
       const int64_t row = static_cast<int64_t>(items[slot].q_row) + t;
       const int piece = items[slot].piece;
       const bool whole = items[slot].pieces == 1;
@@ -788,20 +856,11 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         }
         tc::st_32x32b_x32(tS + 64 + 32 * half, pk);
         l += sum;
-        // V rows z0 .. z1 - 1 have a weight somewhere
-        const int z0 = max(key_lo - kt * kTcKeys, 0), z1 = min(key_hi - kt * kTcKeys, kTcKeys);
-        if (z0 > 0 || z1 < kTcKeys) {
+        if (kt < whole_lo || kt >= whole_hi) {  // clear the V rows that no row of the pair sees
           // (both tiles' warps clear the same rows, each before its own P V)
-          const int vslot = kDeep + (n - 1) % kDeep;
-          if (ok && !rl_wait(bar_full + vslot, ((n - 1) / kDeep) & 1)) ok = false;
-          uint8_t* vt = sm + Lay::kOffRing + vslot * Lay::kTile;
-#pragma unroll 1
-          for (int i = half * kTcRows + r; i < (z0 + kTcKeys - z1) * kSlabs * 8; i += 2 * kTcRows) {
-            const int row = i / (kSlabs * 8), rest = i % (kSlabs * 8);
-            const int at = row < z0 ? row : row - z0 + z1;
-            *reinterpret_cast<uint4*>(vt + (rest >> 3) * Lay::kSlab + at * 128 + (rest & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
+          const int at = (n - 1) % kDeep;
+          if (ok && !rl_wait(bar_full + kDeep + at, ((n - 1) / kDeep) & 1)) ok = false;
+          clear_unseen<D>(sm + Lay::kOffRing + (kDeep + at) * Lay::kTile, seen + at, half * kTcRows + r);
           fence_proxy_async_smem();  // the zeros are read by the tensor cores
         }
         begun = true;

@@ -113,6 +113,16 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
   int first_key = 0, nkeys = ctx + last_row + 1;
   KeySpan span_lo{0, pos_lo + 1}, span_hi{0, pos_hi + 1};
   float slope = 0.f;  // times log2(e)
+  // rules: the keys of tile kt that some row of warp w sees, [kt % 2][w] (a key
+  // between the rows' intervals is not loaded, whatever its value holds)
+  __shared__ uint32_t seen[2][kPfWarps];
+  auto note_seen = [&](int kt) {
+    const int k0 = kt * kPfKeys;
+    static_assert(kPfKeys == 32, "a bit per key of a tile");
+    const uint32_t mine = bits_between(span_lo.lo - k0, span_lo.hi - k0) | bits_between(span_hi.lo - k0, span_hi.hi - k0);
+    const uint32_t all = __reduce_or_sync(0xffffffffu, mine);
+    if (lane == 0) seen[kt & 1][warp] = all;
+  };
   if constexpr (Params::kRules) {
     __shared__ int first, end;
     if (tid == 0) first = INT32_MAX, end = 0;
@@ -134,13 +144,21 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
   }
   const int tile0 = first_key / kPfKeys;
   const int ntiles = (nkeys + kPfKeys - 1) / kPfKeys;
+  if constexpr (Params::kRules) {
+    note_seen(tile0);
+    note_seen(tile0 + 1);
+    __syncthreads();
+  }
 
   auto load_tile = [&](int kt, int stage) {
+    uint32_t keys = 0xffffffffu;
+    if constexpr (Params::kRules) keys = seen[kt & 1][0] | seen[kt & 1][1] | seen[kt & 1][2] | seen[kt & 1][3];
+    static_assert(kPfWarps == 4, "the words of every warp");
     for (int c = tid; c < 2 * kChunks; c += kPfWarps * 32) {
       const int which = c / kChunks, cc = c - which * kChunks;
       const int key = cc / (D / 8), d = (cc % (D / 8)) * 8;
       const int j = kt * kPfKeys + key;
-      const bool valid = j >= first_key && j < nkeys;
+      const bool valid = j < nkeys && (keys >> key & 1u);
       const T* src = static_cast<const T*>(which ? p.v_cache : p.k_cache);
       if (valid) {
         int pb = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq + j / p.block_size);
@@ -172,6 +190,7 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
       cp_async_wait<0>();
     }
     __syncthreads();
+    if constexpr (Params::kRules) note_seen(kt + 2);  // every warp has read this tile's words
     const uint32_t kb = smem_u32(&sm[kt & 1][0][0]), vb = smem_u32(&sm[kt & 1][1][0]);
     // S[16 rows x 32 keys] = Q K^T, four n8 blocks of keys
     float s[4][4];

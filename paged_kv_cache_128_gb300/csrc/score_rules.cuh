@@ -96,6 +96,13 @@ __device__ __forceinline__ KeySpan keys_seen(const ScoreRules& r, int64_t row, i
   return s;
 }
 
+// Bits lo .. hi - 1 of a word, as far as it has them.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return lo < hi ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+}
+
 // c tanh(s / c) log2(e) of a score s = dot * scale: tanh(z) = z P(z^2) for
 // |z| <= 1, P the polynomial of least relative error (4e-9, so float32's
 // rounding is what is left: below 1.1e-7 over the interval), fitted by exchange
