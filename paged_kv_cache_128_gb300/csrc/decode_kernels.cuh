@@ -790,14 +790,17 @@ decode_sk_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ---- prefixes of block counts and costs over the batch (block-wide scans) ----
+  [[maybe_unused]] __shared__ int warp_most[kConsumers + 2];  // rules: most tiles of a sequence
   {
     const int per = (B + kSkThreads - 1) / kSkThreads;
     const int beg = min(B, tid * per), end = min(B, beg + per);
     int local = 0, local_c = 0;
+    [[maybe_unused]] int most = 0;
     for (int i = beg; i < end; ++i) {
       const int Li = checked_len(p, i), lo = first_key(p, i, Li);
       const int nb = lo < Li || !Params::kRules ? (Li + TT - 1) / TT - lo / TT : 0;
       CB[i + 1] = nb;
+      if constexpr (Params::kRules) most = max(most, nb);
       local += nb;
       local_c += nb > 0 ? nb + p.seg_cost : 0;
     }
@@ -816,6 +819,7 @@ decode_sk_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
       warp_tot[warp] = incl;
       warp_tot_c[warp] = incl_c;
     }
+    if constexpr (Params::kRules) warp_most[warp] = __reduce_max_sync(0xffffffffu, most);
     if (tid == 0) CB[0] = CC[0] = 0;
     __syncthreads();
     int base = 0, base_c = 0;
@@ -861,14 +865,20 @@ decode_sk_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
   int P = gridDim.x;
   const int pid = blockIdx.x;
   if constexpr (Params::kRules) {
-    // Few units: at least four tiles a CTA (fewer, and the joining of a unit's
-    // pieces costs more than the tiles), and at most 18 pieces a unit, which one
-    // CTA joins.  Measured, CTAs in all and then by this rule: 8 units of 1 to 4
-    // tiles 14.4 and 10.3 us, of 16 tiles 18.2 and 14.5, of 256 tiles 26.7 and
-    // 22.7; 2 units of 440 tiles 117 and 39; 64 units of 20 tiles alike.
-    const int units = Hkv * ((CC[B] - CB[B]) / p.seg_cost);
-    P = static_cast<int>(min(static_cast<int64_t>(P),
-                             max(static_cast<int64_t>(1), min(static_cast<int64_t>(units) * 18, max(W / 4, static_cast<int64_t>(units))))));
+    // Few units: a CTA takes as many tiles as the longest unit then has pieces,
+    // the square root of its tiles, and four at least (a unit counts as four in
+    // this).  Joining a piece costs its owner what a tile costs a CTA, 0.47 us each
+    // (one unit of 1024 tiles: 304 pieces 168 us, 64 pieces 53), so that this is the
+    // least of the two together.  Measured, on all 304 CTAs, on the best number and
+    // on this rule's (heads of 128, bf16, us): one unit of 64 tiles 44, 18.6 and 19,
+    // of 1024 168, 45 and 45, of 16384 217, 152 and 154; 8 units of 256 tiles 25.9,
+    // 22.6 and 23.1, of 1024 43.4, 43.2 and 43.1; units of 1 and 879 tiles 165, 43
+    // and 43; four times four of 63 and four of 1875 71, 62 and 64.
+    int most = 1;
+    for (int w = 0; w < kConsumers + 2; ++w) most = max(most, warp_most[w]);
+    const int64_t units = static_cast<int64_t>(Hkv) * ((CC[B] - CB[B]) / p.seg_cost);
+    const float want = static_cast<float>(max(W, 4 * units)) / fmaxf(4.f, sqrtf(static_cast<float>(most)));
+    P = max(1, static_cast<int>(fminf(static_cast<float>(P), ceilf(want))));
   }
   auto tiles_before = [&](int64_t x) -> int64_t {  // tiles at cost positions < x
     if (x >= Wc) return W;
