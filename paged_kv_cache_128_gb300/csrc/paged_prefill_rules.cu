@@ -700,9 +700,9 @@ __global__ void __launch_bounds__(kRlThreads, 1)
         float sum;
         // The row's largest score, over both halves (-inf: none has a weight).
         // The cap grows with the score, so that without a bias it is taken of the
-        // largest alone (of the lowest number in the place of -inf, which the cap
-        // gives a weight); with one, every score is capped, by the polynomial unless
-        // one lies beyond it.
+        // largest alone (the lowest number stands for a seen -inf until then, which
+        // the cap gives a weight); with one, every score is capped, by the polynomial
+        // unless one lies beyond it.
         auto row_max = [&]() {
           float m = -INFINITY;
           auto scan = [&](auto in_full) -> bool {
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
           m = fmaxf(m, *row_other);
           named_barrier_sync(pair, 64);  // read before it is written again
           if (CAP && !BIAS && m != -INFINITY)
-            m = soft_cap(m, 1.f, p.rules.cap_log2, __fdiv_rn(1.f, p.rules.cap_log2));
+            m = soft_cap(m == -FLT_MAX ? -INFINITY : m, 1.f, p.rules.cap_log2, __fdiv_rn(1.f, p.rules.cap_log2));
           return m;
         };
         // P = exp2(score - m_ref) rounded to T (keys the row does not see: 0), and

@@ -11,7 +11,7 @@ from tests.rules64 import PagedBatch
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("cap", [0.5, 6.0, 50.0])
+@pytest.mark.parametrize("cap", [0.5, 6.0, 50.0, 1e38])
 @pytest.mark.parametrize("window, sloped", [(1, False), (2, False), (2, True), (9, False)])
 @pytest.mark.parametrize("shape", [("bf16", 8, 2, 128, 16), ("f16", 8, 2, 128, 64), ("f16", 4, 4, 64, 32),
                                    ("bf16", 4, 1, 64, 128), ("f16", 8, 2, 64, 8)], ids=str)
