@@ -509,8 +509,9 @@ int paged_prefill_attention(void* out, const void* q, const void* k_cache, const
  *   key_begin) and hi = min(L, key_end, or i + 1 without key_end);
  *   out = sum_{j seen} softmax_j(s_ij) V_j, and zeros where nothing is seen.
  *   softcap: 0 (none) or a positive finite cap; scale / softcap and
- *     softcap log2(e) must be float32 numbers.
- *   slopes: device float32[num_heads], finite, or NULL.
+ *     softcap log2(e) must be float32 numbers, the latter no subnormal one.
+ *   slopes: device float32[num_heads], of either sign, or NULL; the products of
+ *     slopes log2(e) and distances must be float32 numbers.
  *   window: 0 (all) or the number of keys seen up to and with the own one.
  *   key_begin, key_end: device int32[query rows], any values, or NULL.
  * A key that a query does not see takes no part in its row, whatever K holds

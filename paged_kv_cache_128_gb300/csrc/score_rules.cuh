@@ -9,6 +9,7 @@
 // Scores are held in the exp2 domain (times log2 e), as everywhere here.
 #pragma once
 
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -61,8 +62,8 @@ inline int make_rules(float scale, float softcap, const float* slopes, int32_t w
   if (softcap > 0.f) {
     r.cap_log2 = softcap * kLog2e;
     r.cap_arg = scale / softcap;
-    // a cap so large or small that these leave float32
-    if (!std::isfinite(r.cap_log2) || !(r.cap_log2 > 0.f) || !std::isfinite(r.cap_arg)) return KV_ERR_INVALID_ARG;
+    // a cap so large or small that these, or the former's reciprocal, leave float32
+    if (!std::isfinite(r.cap_log2) || !(r.cap_log2 >= FLT_MIN) || !std::isfinite(r.cap_arg)) return KV_ERR_INVALID_ARG;
     constexpr float k[6] = {0.9999994039535522f,    -0.3332904279232025f,  0.13281433284282684f,
                             -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
     // Where a^2 is so small that a^10 would leave float32 (a cap over 3000 times
