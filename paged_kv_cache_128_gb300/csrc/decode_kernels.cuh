@@ -103,8 +103,8 @@ struct DecodeParams {
 
 // The same with score rules (score_rules.cuh), with and without a cap; the
 // kernels are compiled for each of the three.  (With the cap's test at run time
-// the fp8 kernel was a quarter slower without one, 194 us for 136: its code no
-// longer stayed in the instruction cache.)
+// the fp8 kernel took 171 us for 123 without one, 121 sequences in stretches of
+// 8192: its code no longer stayed in the instruction cache.)
 template <bool CAP>
 struct RulesParams : DecodeParams {
   static constexpr bool kRules = true, kCap = CAP;

@@ -5,9 +5,9 @@
 // before that key are not looked up; scores pass through the cap and the
 // distance bias before the online softmax.  What bounds it: memory, as the plain
 // calls; fp8 caches their consumers' instructions.  Measured: 64 sequences to
-// 16384 tokens, window 4096, cap 30, 32/8 heads of 128: 174 us, 1075 MB (0.92 of
-// the copy rate); 32 to 8192, cap 50, 16/8 heads of 256: 208 us, 1308 MB (0.94);
-// fp8, 121 sequences, stretches of 8192, 28/4 heads: 124 us, 536 MB (0.65; a
+// 16384 tokens, window 4096, cap 30, 32/8 heads of 128: 176 us, 1075 MB (0.92 of
+// the copy rate); 32 to 8192, cap 50, 16/8 heads of 256: 209 us, 1308 MB (0.94);
+// fp8, 121 sequences, stretches of 8192, 28/4 heads: 123 us, 536 MB (0.65; a
 // copy of the kernel that only loads takes 103).  Here without a cap; with one in
 // paged_decode_rules_cap.cu.
 

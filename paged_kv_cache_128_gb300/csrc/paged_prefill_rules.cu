@@ -46,12 +46,13 @@ namespace {
 // Where few rows see many keys an item's key tiles are cut into pieces, whose
 // parts join_pieces_kernel joins.
 //
-// What bounds it: per key tile and pair, the chain S (500 cycles), softmax
-// (1100; with a cap 2200), P V (650), whose gaps the other query tile's products
-// fill: some 3300 cycles, of which the tensor cores work 2050.  Measured: 8192
-// causal tokens of 32/8 heads of 128, bf16: 436 us, 1.26 PFLOP/s of the keys
-// seen (0.67 of the measured peak), with a cap 513, with a bias 457, with both
-// 627; a chunk of 8192 under a window of 4096, 28/4 heads: 393 us, 1.22 PFLOP/s.
+// What bounds it: no pipe alone.  A key tile costs a pair some 3300 cycles, of
+// which the tensor cores work 2050; the chain of one query tile, S (500), softmax
+// (1100; with a cap 2200) and P V (650), is 2250 long and the two run side by side,
+// so that a thousand cycles are accounted for by neither.  Measured: 8192 causal
+// tokens of 32/8 heads of 128, bf16: 428 us, 1.28 PFLOP/s of the keys seen (0.68 of
+// the measured peak), with a cap 517, with a bias 460, with both 628; a chunk of
+// 8192 under a window of 4096, 28/4 heads: 388 us, 1.24 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kRlSoftWarps = 8;  // per query tile: a row's keys are halved between two warps
 constexpr int kRlMmaWarp = 2 * kRlSoftWarps, kRlTmaWarp = kRlMmaWarp + 1, kRlValueWarp = kRlTmaWarp + 1;
@@ -987,10 +988,12 @@ int device_sms() {
 // Pieces that each item's keys may be cut into: the number of least cost for
 // the most items and tiles that the arguments allow for (the lengths are on the
 // device, where the scheduler decides by them, up to this number).  Measured,
-// 32/8 heads of 128, whole and in pieces: 40 rows after 20000 tokens 445 and 50
-// us (19 pieces), 64 after 2000 43 and 27 (8), 300 after 4000 105 and 62 (4), 1000
-// after 8000 209 and 159 (2); 2600 causal rows of 16/2 heads 60, and 79 in 3
-// pieces, which this cost does not call for.  Calls that give key_begin are not
+// 32/8 heads of 128, whole and in pieces: 40 rows after 20000 tokens 449 and 50
+// us (19 pieces), 64 after 2000 41 and 27 (8), 300 after 4000 107 and 60 (4), 1000
+// after 8000 210 and 156 (2); 2600 causal rows of 16/2 heads 60, and 79 in 3
+// pieces, which this cost does not call for.  It counts on the mean of the CTAs and
+// not on whole rounds of them: 8 chunks to 128 rows after to 1000 tokens take 37 us
+// whole, and 50 in the two pieces that it asks for behind a wide table.  Calls that give key_begin are not
 // cut: what their rows see has little to do with the lengths.
 struct RlPlan {
   int hg_log2, splits;

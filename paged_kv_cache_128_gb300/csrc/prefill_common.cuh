@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(kPfWarps * 32) prefill_kernel(const Params p) 
   const int tile0 = first_key / kPfKeys;
   const int ntiles = (nkeys + kPfKeys - 1) / kPfKeys;
   if constexpr (Params::kRules) {
-    note_seen(tile0);
-    note_seen(tile0 + 1);
+    if (tile0 < ntiles) {
+      note_seen(tile0);
+      note_seen(tile0 + 1);
+    }
     __syncthreads();
   }
 

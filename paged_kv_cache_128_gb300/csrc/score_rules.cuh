@@ -66,9 +66,9 @@ inline int make_rules(float scale, float softcap, const float* slopes, int32_t w
     if (!std::isfinite(r.cap_log2) || !(r.cap_log2 >= FLT_MIN) || !std::isfinite(r.cap_arg)) return KV_ERR_INVALID_ARG;
     constexpr float k[6] = {0.9999994039535522f,    -0.3332904279232025f,  0.13281433284282684f,
                             -0.051605675369501114f, 0.016743117943406105f, -0.0030670613050460815f};
-    // Where a^2 is so small that a^10 would leave float32 (a cap over 3000 times
-    // the scale, which scores hardly come near to) nothing is in range and the
-    // exact form serves.
+    // Where a^2 is so small that a^10 would leave float32 (a cap over 3162 times
+    // the scale: 50 with a scale of 1/128, say) nothing is in range and every score
+    // takes the exact form, at a cost in time.
     const double a2 = static_cast<double>(r.cap_arg) * r.cap_arg;
     const bool fits = a2 >= 1e-7 && a2 <= 1e7;
     double power = static_cast<double>(scale) * kLog2e;
